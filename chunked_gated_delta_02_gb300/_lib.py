@@ -18,6 +18,8 @@ _lib = None
 P = ctypes.c_void_p
 I = ctypes.c_int
 F = ctypes.c_float
+L = ctypes.c_int64
+U = ctypes.c_uint32
 
 STATUS = {0: "KDA_OK", 1: "KDA_ERR_INVALID_ARG", 2: "KDA_ERR_UNSUPPORTED", 3: "KDA_ERR_WORKSPACE",
           4: "KDA_ERR_CUDA", 5: "KDA_ERR_DEVICE_STATUS"}
@@ -33,6 +35,12 @@ SIGNATURES = {
                         P, P]),
     "kda_fwd_noalloc": (I, [P, P, P, P, P, P, P, F, F, P, P, P, I, I, I, I, I, I, P, P]),
     "kda_debug_chunk_matrices": (I, [P, P, P, P, P, P, F, P, I, I, I, I, I, P, P, ctypes.c_size_t, P]),
+    "kda_step": (I, [P, P, P, P, P, P, P, F, F, P, P, I, I, I, I, L, P, U, P, P]),
+    "kda_la_workspace_size": (ctypes.c_size_t, [I, I, I, I, I, I, I]),
+    "kda_la_fwd": (I, [P, P, P, P, F, P, P, P, I, I, I, I, I, I, I, P, U, P, P, ctypes.c_size_t, P]),
+    "kda_la_step": (I, [P, P, P, P, F, P, P, I, I, I, I, I, L, P, U, P, P]),
+    "kda_norm_gate": (I, [P, P, P, F, L, L, I, P, U, P, P]),
+    "kda_add_norm": (I, [P, P, P, P, P, P, F, F, L, I, P, U, P, P, P]),
     "kda_max_chunks": (ctypes.c_int64, [I, I, I]),
     "kda_fwd_plan": (I, [I, I, I, I, I, I, I, ctypes.c_uint32, ctypes.POINTER(I), ctypes.POINTER(I)]),
     "kda_status_string": (ctypes.c_char_p, [I]),

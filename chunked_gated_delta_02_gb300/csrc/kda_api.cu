@@ -10,6 +10,7 @@
 
 #include "../../include/kda.h"
 #include "kda_common.cuh"
+#include "kda_host.cuh"
 #include "umma.cuh"
 
 namespace kda {
@@ -23,7 +24,6 @@ cudaError_t launch_recur_segments(const Problem &p, const TmaMaps &maps, int pas
 cudaError_t launch_cp_combine(const Problem &p, cudaStream_t stream);
 int recur_slice_width(const Problem &p);
 int slice_width_for(long long N, int H, int V, int sms);
-int device_sm_count();
 int cp_max_segments(int T, int H, int V, int N, bool varlen, uint32_t cp_flags);
 int cp_auto_segments(int T, int H, int K, int V, int N, int sms, int n_max, int plain_bv);
 }  // namespace kda
@@ -43,11 +43,8 @@ static __global__ void wait_timeout_kernel(long long limit) {
     atomicExch(&g_kda_device_status, kda::kDevWaitTimeout);
 }
 
-// NVTX range for the host-side enqueue of one stage (shows up around the launches in a trace).
-struct NvtxRange {
-  explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-};
+using kda::NvtxRange;
+using kda::aligned;
 
 namespace {
 
@@ -90,8 +87,6 @@ Layout layout_of(int B, int T, int H, int K, int V, int N, int n_seg_max) {
   L.total = off;
   return L;
 }
-
-bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
 
 // cuTensorMapEncodeTiled from the driver, looked up once through the runtime.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -234,26 +229,8 @@ kda_status_t fill_problem(kda::Problem &p, const Layout &L, void *ws, const void
   p.n_seg = 0;
   p.mats = reinterpret_cast<__half *>(p.hand);
   p.mat_stride = p.hand_stride / 2;
-  static kda::PerDeviceOnce once;
-  static std::atomic<int *> status_addr[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
-  const cudaError_t e = once([&](int d) {
-    int *a = nullptr;
-    const cudaError_t r = cudaGetSymbolAddress(reinterpret_cast<void **>(&a), g_kda_device_status);
-    if (r == cudaSuccess && d >= 0 && d < 64) status_addr[d].store(a, std::memory_order_relaxed);
-    return r;
-  });
-  p.dev_status = (dev >= 0 && dev < 64) ? status_addr[dev].load(std::memory_order_relaxed) : nullptr;
-  if (e == cudaSuccess && !p.dev_status &&
-      cudaGetSymbolAddress(reinterpret_cast<void **>(&p.dev_status), g_kda_device_status) != cudaSuccess) {
-    cudaGetLastError();
-    return KDA_ERR_CUDA;
-  }
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return KDA_ERR_CUDA;
-  }
+  p.dev_status = kda::device_status_address();
+  if (!p.dev_status) return KDA_ERR_CUDA;
   p.lb = lower_bound;
   p.scale = scale;
   p.B = B;
@@ -268,6 +245,45 @@ kda_status_t fill_problem(kda::Problem &p, const Layout &L, void *ws, const void
 }
 
 }  // namespace
+
+namespace kda {
+
+int *device_status_address() {
+  static PerDeviceOnce once;
+  static std::atomic<int *> status_addr[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  const cudaError_t e = once([&](int d) {
+    int *a = nullptr;
+    const cudaError_t r = cudaGetSymbolAddress(reinterpret_cast<void **>(&a), g_kda_device_status);
+    if (r == cudaSuccess && d >= 0 && d < 64) status_addr[d].store(a, std::memory_order_relaxed);
+    return r;
+  });
+  int *addr = (dev >= 0 && dev < 64) ? status_addr[dev].load(std::memory_order_relaxed) : nullptr;
+  if (e != cudaSuccess || (!addr && cudaGetSymbolAddress(reinterpret_cast<void **>(&addr), g_kda_device_status) !=
+                                        cudaSuccess)) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  return addr;
+}
+
+bool encode_swizzled_token_map(CUtensorMap *m, const void *base, int D, int H, int T, int B,
+                               const long long (&stride_bytes)[3], int rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+  // the stride of a dimension of one entry is never used, but has to be a valid one
+  cuuint64_t strides[3];
+  for (int i = 0; i < 3; ++i) strides[i] = dims[i + 1] == 1 ? (cuuint64_t)D * 2 : (cuuint64_t)stride_bytes[i];
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace kda
 
 extern "C" {
 

@@ -29,6 +29,7 @@ constexpr int kDevOk = 0;
 constexpr int kDevBadCuSeqlens = 1;
 constexpr int kDevWaitTimeout = 2;
 constexpr int kDevNonFinite = 3;     // the recurrence's last state of a (sequence, head) is not finite
+constexpr int kDevBadStateIndex = 4; // a state index of a single-token call lies outside the pool
 
 // Variant flags (mirrors KDA_GATE_PER_HEAD, KDA_BETA_F32, KDA_STATE_BF16, KDA_STATE_KV in
 // include/kda.h).
@@ -42,6 +43,8 @@ constexpr uint32_t kExp2Poly = 0x10u;     // per-token decays 2^la by a polynomi
 constexpr uint32_t kCpOff = 0x20u;
 constexpr int kCpSegShift = 8;
 constexpr uint32_t kCpFlagsMask = kCpOff | (0xFFu << kCpSegShift);
+// Linear attention (mirrors KDA_LA_TOKEN_DECAY in include/kda.h): one log decay per token and head.
+constexpr uint32_t kLaTokenDecay = 0x10000u;
 
 struct Problem {
   const __nv_bfloat16 *q, *k, *v, *g;  // g [B,T,H,K], or [B,T,H] with kGatePerHead

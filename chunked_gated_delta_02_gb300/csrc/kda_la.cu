@@ -1,0 +1,1030 @@
+// Linear attention with one decay per head, chunked form, on the 5th-generation tensor cores
+// (tcgen05, accumulators in tensor memory).
+//
+// Per sequence and head, for tokens t in order (S is K x V, a_t <= 0 the log decay):
+//   S_t = exp(a_t) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+// With chunks of C = 128 tokens and G_i the sum of the log decays of the chunk up to token i:
+//   o_i = scale (sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j + exp(G_i) S^T q_i)
+//   S   = exp(G_C) S + sum_j exp(G_C - G_j) k_j v_j^T
+// as four products per chunk:
+//   M1: scores = Q K^T               C x C,  both operands in shared memory
+//   M2: O      = Q S                 C x V,  S in bf16
+//   M3: O     += P V                 C x V,  P the masked scores times exp(G_i - G_j - R_i), in bf16
+//   M4: D^T    = V'^T K              V x K,  V' = v_j exp(G_C - G_j) as a sum of three bf16 terms
+//   o_i = scale exp(R_i) O_i,  S^T = exp(G_C) S^T + D^T in fp32, in registers for the whole sequence
+//
+// R_i = max(G_i, -64 ln 2) takes the row's decay out of P, so that M2 and M3 can add into one
+// accumulator and an element of P costs one factor of its column, exp(-G_j). Where the decay of a
+// chunk goes below 2^-64, G_i - G_j - R_i stays within (-inf, 64 ln 2] and is formed pairwise; rows
+// that far down take 2^-64 Q S instead of less, which is below the rounding of anything else.
+//
+// What is rounded: q, k and v are exact (bf16 inputs). P and the copy of S that M2 reads are bf16,
+// like the output they go to: each adds about as much error as the rounding of o itself. The state
+// is fp32 and has to stay fp32-accurate over a whole sequence, so its only rounded operand, V', is
+// split into three bf16 terms, which hold all 24 bits: with two the state's error against fp64 was
+// 2.7e-6, more than ten times that of fp32 arithmetic.
+//
+// A CTA takes (sequence segment, head) items, all V columns at once, so that q, k and v are read
+// once; it is persistent over items (one CTA per SM: two stages of q, k and v and S fill the
+// shared memory). Warp roles, coupled by mbarriers only:
+//   warps 0-3    P, in place of the scores in tensor memory (A operand of M3)
+//   warps 4-7    V': transposed from the v tile into tensor memory (A operand of M4), 32 tokens at
+//                a time into two buffers in turn
+//   warps 8-15   the state, and the scaled output in bf16
+//   warp 16      loads (TMA, 128-byte swizzle) and the chunk's decay factors
+//   warp 17      issues M1, M2 and M3;  warp 18  issues M4
+//   warp 19      stores the output tile, which the state warps leave in the chunk's v buffer
+// V' as the tensor-memory operand makes D^T come out with one value column per lane, the layout in
+// which a thread can update its part of S^T and write it as rows of M2's operand without transposing.
+//
+// Bound: a chunk of one head moves 128 KiB at K = V = 128, 2.9 us of an SM's share of the measured
+// bandwidth, against 48 tensor-core steps of 64 clocks, 1.6 us: memory bandwidth, if loads, products
+// and register work overlap.
+#include <cmath>
+#include <cstring>
+
+#include "../../include/kda.h"
+#include "kda_host.cuh"
+#include "kda_la.cuh"
+#include "umma.cuh"
+
+namespace kda {
+
+constexpr int kLaThreads = 640;
+// Registers per thread by warpgroup; a block is launched with 96 for each of its threads, and the
+// state warps' increase is what the others give back: 2 x 32 = 8 + 8 + 48.
+constexpr int kLaRegsP = 88, kLaRegsV = 88, kLaRegsState = 128, kLaRegsIssue = 48;
+static_assert(kLaRegsP + kLaRegsV + 2 * kLaRegsState + kLaRegsIssue <= 5 * 96, "registers at launch");
+constexpr uint32_t kLaTmemCols = 512;
+constexpr long long kLaWaitLimit = 4000000000LL;   // ~2 s of SM clocks per wait
+// The smallest log2 decay of a token: 2^-126 is the smallest normal fp32 number, so that a decay of
+// zero (log decay -inf) drops the state without an inf - inf in the sums.
+constexpr float kLaMinLog2 = -126.0f;
+// Row decays below 2^-64 stay in P (see above): 2^64 leaves the scores and values as much range again.
+constexpr float kLaRowLog2 = -64.0f;
+
+// Decay factors of one chunk.
+struct LaGate {
+  float G[kLaChunk];    // log2 decay from the chunk's start through token i
+  float cf[kLaChunk];   // decay from token j to the end of its 32-token block; 0 past the sequence
+  float bf[4];          // decay from the end of 32-token block c to the chunk's end
+  float gamma;          // decay of the whole chunk
+  float pad[3];
+};
+
+struct LaMisc {
+  // per stage: q, k and the decay factors ready and consumed; the same of v, whose buffer then holds
+  // the output tile; v rows past the sequence cleared; output tile written
+  uint64_t full[3], empty[3], full_v[3], empty_v[3], v_rdy[3], o_st[3];
+  uint64_t p_raw, p_rdy, s_free, o_done, o_free, d_rdy, d_free, s_rdy;   // one phase per chunk
+  uint64_t vp_rdy[2], vp_free[2];                   // per V' buffer: 32 tokens ready, read
+  uint64_t bar_exit;
+  uint32_t tmem_slot;
+  int err;
+};
+
+template <int K, int V, bool AGG>
+struct LaLayout {
+  static constexpr uint32_t panel = kLaChunk * 128;   // 128 tokens x 64 columns
+  static constexpr uint32_t k_off = AGG ? 0 : (K / 64) * panel;
+  static constexpr uint32_t v_off = k_off + (K / 64) * panel;
+  static constexpr uint32_t stage = v_off + (V / 64) * panel;
+  static constexpr int stages = AGG ? 3 : 2;
+  static constexpr uint32_t s_off = stages * stage;                 // S^T rows v, bf16, K-major panels
+  static constexpr uint32_t s_panel = V * 128;
+  static constexpr uint32_t gate = s_off + (AGG ? 0 : (K / 64) * s_panel);
+  static constexpr uint32_t misc = gate + stages * (uint32_t)sizeof(LaGate);
+  static constexpr uint32_t bytes = misc + (uint32_t)sizeof(LaMisc);
+  static_assert(bytes <= 232448, "shared memory of one CTA");
+};
+
+// Tensor memory columns.
+constexpr uint32_t kTmP = 0;      // scores, 128 fp32; P takes the first 64 (bf16 pairs)
+constexpr uint32_t kTmVp = 128;   // V'^T: two buffers of 32 tokens, three terms of 16 columns each
+constexpr uint32_t kTmVpBuf = 48;
+constexpr uint32_t kTmO = 256;    // O, V columns
+constexpr uint32_t kTmD = 384;    // D^T, K columns
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&x);
+}
+
+__device__ __forceinline__ LaItem la_item(const LaProblem &p, long long idx) {
+  LaItem it;
+  if (p.cu) {
+    it = p.items[idx];
+  } else {
+    const int s = (int)(idx / p.n_seg), g = (int)(idx % p.n_seg);
+    it.seq = s;
+    it.b = s;
+    it.t0 = g * p.seg_chunks * kLaChunk;
+    it.len = max(0, min(p.T - it.t0, p.seg_chunks * kLaChunk));
+    it.slot = (int)idx;
+    it.seg = g;
+    it.n_seg = p.n_seg;
+  }
+  return it;
+}
+
+// S^T row v of (sequence s, head h), columns [k0, k0 + N): to and from the caller's state.
+template <int K, int V, int N>
+__device__ __forceinline__ void la_state_load(const LaProblem &p, int s, int h, int v, int k0, float (&S)[N]) {
+  const long long base = ((long long)s * p.H + h) * K * V;
+  if (p.flags & kStateKV) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const long long i = base + (long long)(k0 + j) * V + v;
+      S[j] = (p.flags & kStateBf16) ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.init)[i])
+                                    : static_cast<const float *>(p.init)[i];
+    }
+  } else if (p.flags & kStateBf16) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.init) + base + (long long)v * K + k0);
+#pragma unroll
+    for (int j = 0; j < N / 8; ++j) {
+      const uint4 r = src[j];
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        S[8 * j + 2 * e] = __uint_as_float(w[e] << 16);
+        S[8 * j + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+    }
+  } else {
+    const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.init) + base + (long long)v * K + k0);
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) {
+      const float4 f = src[j];
+      S[4 * j] = f.x; S[4 * j + 1] = f.y; S[4 * j + 2] = f.z; S[4 * j + 3] = f.w;
+    }
+  }
+}
+template <int K, int V, int N>
+__device__ __forceinline__ void la_state_store(const LaProblem &p, int s, int h, int v, int k0, const float (&S)[N]) {
+  const long long base = ((long long)s * p.H + h) * K * V;
+  if (p.flags & kStateKV) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const long long i = base + (long long)(k0 + j) * V + v;
+      if (p.flags & kStateBf16) static_cast<__nv_bfloat16 *>(p.final_state)[i] = __float2bfloat16_rn(S[j]);
+      else static_cast<float *>(p.final_state)[i] = S[j];
+    }
+  } else if (p.flags & kStateBf16) {
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.final_state) + base + (long long)v * K + k0);
+#pragma unroll
+    for (int j = 0; j < N / 8; ++j)
+      dst[j] = make_uint4(pack_bf16(S[8 * j], S[8 * j + 1]), pack_bf16(S[8 * j + 2], S[8 * j + 3]),
+                          pack_bf16(S[8 * j + 4], S[8 * j + 5]), pack_bf16(S[8 * j + 6], S[8 * j + 7]));
+  } else {
+    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.final_state) + base + (long long)v * K + k0);
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) dst[j] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+  }
+}
+
+// Segment states: float4 j of thread (half, v) at [j][half V + v], so that warps read and write
+// 512 contiguous bytes. Column k = half K / 2 + 4 j + e.
+template <int K, int V>
+__device__ __forceinline__ long long la_seg_index(int half, int v, int j) {
+  return ((long long)j * (2 * V) + half * V + v) * 4;
+}
+
+// AGG: only the state that each segment adds, started from zero (segments before the last of their
+// sequence). Otherwise everything, from the segment's start state.
+template <int K, int V, bool AGG>
+__global__ void __launch_bounds__(kLaThreads, 1)
+la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
+  using Lay = LaLayout<K, V, AGG>;
+  constexpr int kStages = Lay::stages;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  LaMisc &ms = *reinterpret_cast<LaMisc *>(sm + Lay::misc);
+  LaGate *gates = reinterpret_cast<LaGate *>(sm + Lay::gate);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t sbase = umma::smem_u32(sm);
+  pdl_wait();   // the schedule, the segment states (when launched to overlap their kernels)
+  if (p.flag && *p.flag != kDevOk) return;
+  if (sbase & 1023u) {   // the operand layouts need it; never the case for a kernel without static shared memory
+    if (tid == 0) atomicExch(p.dev_status, kDevWaitTimeout);
+    return;
+  }
+  const long long total = (p.cu ? (long long)*p.n_items : (long long)p.N * p.n_seg) * p.H;
+
+  if (warp == 0) {
+    umma::tmem_alloc(&ms.tmem_slot, kLaTmemCols);
+    umma::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      umma::mbar_init(&ms.v_rdy[s], 4);
+      umma::mbar_init(&ms.full[s], 2);        // the loads' issuer and the factors' writer
+      umma::mbar_init(&ms.empty[s], (AGG ? 1 : 2) + 8);   // M4, M3 and the eight state warps
+      umma::mbar_init(&ms.full_v[s], 1);
+      umma::mbar_init(&ms.empty_v[s], 1);
+      umma::mbar_init(&ms.o_st[s], 8);
+    }
+    for (int b = 0; b < 2; ++b) {
+      umma::mbar_init(&ms.vp_rdy[b], 4);
+      umma::mbar_init(&ms.vp_free[b], 1);
+    }
+    umma::mbar_init(&ms.p_raw, 1);
+    umma::mbar_init(&ms.p_rdy, 4);
+    umma::mbar_init(&ms.s_free, 1);
+    umma::mbar_init(&ms.o_done, 1);
+    umma::mbar_init(&ms.o_free, 8);
+    umma::mbar_init(&ms.d_rdy, 1);
+    umma::mbar_init(&ms.d_free, 8);
+    umma::mbar_init(&ms.s_rdy, 8);
+    umma::mbar_init(&ms.bar_exit, 2);
+    umma::mbar_fence_init();
+    ms.err = 0;
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tmem = ms.tmem_slot;
+  const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+  const int row = (warp & 3) * 32 + lane;   // this thread's tensor memory lane
+
+  // Bounded wait of one thread; it ends early once any wait of the CTA has given up.
+  auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool {
+    if (umma::mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!umma::mbar_try_wait(bar, parity)) {
+      if (*(volatile int *)&ms.err) return false;
+      if (clock64() - t0 > kLaWaitLimit) {
+        atomicExch(&ms.err, 1);
+        return false;
+      }
+    }
+    return true;
+  };
+  // The same for a whole warp, with one answer.
+  auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+    const bool ok = __all_sync(0xffffffffu, wait1(bar, parity));
+    umma::fence_after_sync();
+    return ok;
+  };
+  // One arrival for the warp after its tensor memory or shared memory accesses.
+  auto arrive = [&](uint64_t *bar) {
+    umma::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) umma::mbar_arrive(bar);
+  };
+  // f(item, head, n): every chunk of this CTA's items, n counting them over all items; begin(item,
+  // head, chunks) and end(item, head, chunks) around them. All stop at the first false.
+  auto for_chunks = [&](auto &&begin, auto &&chunk, auto &&end) {
+    int n = 0;
+    for (long long w = blockIdx.x; w < total; w += gridDim.x) {
+      const LaItem it = la_item(p, w / p.H);
+      const int h = (int)(w % p.H);
+      if (AGG && it.seg == it.n_seg - 1) continue;
+      const int nch = (it.len + kLaChunk - 1) / kLaChunk;
+      if (!begin(it, h, nch)) return;
+      for (int c = 0; c < nch; ++c, ++n)
+        if (!chunk(it, h, c, nch, n)) return;
+      if (!end(it, h, nch)) return;
+    }
+  };
+  auto nothing = [](const LaItem &, int, int) { return true; };
+
+  if (warp >= 16) umma::regs_dec<kLaRegsIssue>();
+  if (warp == 16) {
+    // ======================= loads and decay factors =======================
+    const int hq_group = p.H / p.Hk;
+    int issued = 0, issued_v = 0;
+    for_chunks(nothing, [&](const LaItem &it, int h, int c, int, int n) {
+      const int st = (int)(n % kStages);
+      const uint32_t ph = (uint32_t)((n / kStages) & 1);
+      if (n >= kStages && !wait(&ms.empty[st], ph ^ 1u)) return false;
+      const int t0 = it.t0 + c * kLaChunk, L = min(kLaChunk, it.len - c * kLaChunk);
+      if (umma::elect_one()) {
+        unsigned char *dst = sm + st * Lay::stage;
+        umma::mbar_arrive_expect_tx(&ms.full[st], Lay::v_off);
+        const int hq = h / hq_group;
+        if constexpr (!AGG)
+          for (int x = 0; x < K / 64; ++x) umma::tma_load_4d(dst + x * Lay::panel, &maps.q, x * 64, hq, t0, it.b, &ms.full[st]);
+        for (int x = 0; x < K / 64; ++x) umma::tma_load_4d(dst + Lay::k_off + x * Lay::panel, &maps.k, x * 64, hq, t0, it.b, &ms.full[st]);
+      }
+      // Lane l: tokens 4 l .. 4 l + 3; lanes 8 c .. 8 c + 7 are 32-token block c.
+      float a[4], pre[4], suf[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 4 * lane + e;
+        float x = 0.f;
+        if (i < L) {
+          x = (p.flags & kLaTokenDecay) ? p.decay[it.b * p.ds[0] + (long long)(t0 + i) * p.ds[1] + h * p.ds[2]] : p.decay[h];
+          x *= kLog2e;
+          x = x < kLaMinLog2 ? kLaMinLog2 : x;   // NaN stays
+        }
+        a[e] = x;
+      }
+      pre[0] = a[0];
+      suf[3] = 0.f;
+#pragma unroll
+      for (int e = 1; e < 4; ++e) {
+        pre[e] = pre[e - 1] + a[e];
+        suf[3 - e] = suf[4 - e] + a[4 - e];
+      }
+      float incl = pre[3];   // sums through this lane
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, incl, m);
+        if (lane >= m) incl += y;
+      }
+      float before = __shfl_up_sync(0xffffffffu, incl, 1);
+      if (lane == 0) before = 0.f;
+      // sums over the later lanes of the block, formed from the block's end so that small sums
+      // near the end keep their precision
+      float after = pre[3];
+#pragma unroll
+      for (int m = 1; m < 8; m <<= 1) {
+        const float y = __shfl_down_sync(0xffffffffu, after, m);
+        if ((lane & 7) + m < 8) after += y;
+      }
+      const float block = __shfl_sync(0xffffffffu, after, lane & 24);   // the block's total
+      const float later = __shfl_down_sync(0xffffffffu, after, 1);
+      const float tail = (lane & 7) == 7 ? 0.f : later;
+      LaGate &g = gates[st];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 4 * lane + e;
+        g.G[i] = before + pre[e];
+        g.cf[i] = i < L ? ex2_approx(suf[e] + tail) : 0.f;
+      }
+      const float b1 = __shfl_sync(0xffffffffu, block, 8), b2 = __shfl_sync(0xffffffffu, block, 16),
+                  b3 = __shfl_sync(0xffffffffu, block, 24), b0 = __shfl_sync(0xffffffffu, block, 0);
+      if (lane == 0) {
+        g.bf[0] = ex2_approx(b1 + b2 + b3);
+        g.bf[1] = ex2_approx(b2 + b3);
+        g.bf[2] = ex2_approx(b3);
+        g.bf[3] = 1.f;
+        g.gamma = ex2_approx(b0 + b1 + b2 + b3);
+      }
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(&ms.full[st]);
+      issued = n + 1;
+      if (n >= kStages && !wait(&ms.empty_v[st], ph ^ 1u)) return false;
+      if (umma::elect_one()) {
+        umma::mbar_arrive_expect_tx(&ms.full_v[st], Lay::stage - Lay::v_off);
+        for (int x = 0; x < V / 64; ++x)
+          umma::tma_load_4d(sm + st * Lay::stage + Lay::v_off + x * Lay::panel, &maps.v, x * 64, h, t0, it.b, &ms.full_v[st]);
+      }
+      issued_v = n + 1;
+      return true;
+    }, nothing);
+    // after a timeout: wait (bounded) for the copies in flight
+    if (lane == 0 && *(volatile int *)&ms.err) {
+      for (int n = max(0, issued - kStages); n < issued; ++n)
+        umma::mbar_wait_bounded(&ms.full[n % kStages], (uint32_t)((n / kStages) & 1), kLaWaitLimit);
+      for (int n = max(0, issued_v - kStages); n < issued_v; ++n)
+        umma::mbar_wait_bounded(&ms.full_v[n % kStages], (uint32_t)((n / kStages) & 1), kLaWaitLimit);
+    }
+  } else if (warp == 17) {
+    // ======================= M1, M2, M3 =======================
+    if constexpr (!AGG) {
+      constexpr uint32_t id1 = umma::idesc_bf16(128, 128, 0, 0), id2 = umma::idesc_bf16(128, V, 0, 0);
+      constexpr uint32_t id3 = umma::idesc_bf16(128, V, 0, 1);
+      const uint64_t bs = umma::sdesc_sw128(sbase + Lay::s_off, 16, 1024);
+      for_chunks(nothing, [&](const LaItem &, int, int, int, int n) {
+        const int st = n % kStages;
+        const uint32_t ph = (uint32_t)(n & 1), sph = (uint32_t)((n / kStages) & 1), q0 = sbase + st * Lay::stage;
+        const uint64_t aq = umma::sdesc_sw128(q0, 16, 1024), bk = umma::sdesc_sw128(q0 + Lay::k_off, 16, 1024);
+        const uint64_t bv = umma::sdesc_sw128(q0 + Lay::v_off, Lay::panel, 1024);
+        if (!wait(&ms.full[st], sph)) return false;
+        // M1: scores = Q K^T (the scores of the chunk before were last read by its M3, ahead of this in order)
+        if (umma::elect_one()) {
+#pragma unroll
+          for (int x = 0; x < K / 16; ++x) {
+            const uint32_t off = (x / 4) * Lay::panel + (x % 4) * 32;
+            umma::mma_f16_ss(tmem + kTmP, umma::desc_add(aq, off), umma::desc_add(bk, off), id1, x > 0);
+          }
+          umma::commit(&ms.p_raw);
+        }
+        // M2: O = Q S
+        if (!wait(&ms.s_rdy, ph)) return false;
+        if (n > 0 && !wait(&ms.o_free, ph ^ 1u)) return false;
+        if (umma::elect_one()) {
+#pragma unroll
+          for (int x = 0; x < K / 16; ++x)
+            umma::mma_f16_ss(tmem + kTmO, umma::desc_add(aq, (x / 4) * Lay::panel + (x % 4) * 32),
+                             umma::desc_add(bs, (x / 4) * Lay::s_panel + (x % 4) * 32), id2, x > 0);
+          umma::commit(&ms.s_free);
+        }
+        // M3: O += P V; v_rdy: rows of the v tile past the sequence have been cleared
+        if (!wait(&ms.v_rdy[st], sph) || !wait(&ms.p_rdy, ph)) return false;
+        if (umma::elect_one()) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            umma::mma_f16_ts(tmem + kTmO, tmem + kTmP + x * 8, umma::desc_add(bv, x * 2048), id3, 1);
+          umma::commit(&ms.o_done);
+          umma::commit(&ms.empty[st]);
+        }
+        __syncwarp();
+        return true;
+      }, nothing);
+    }
+    if (umma::elect_one()) umma::commit(&ms.bar_exit);   // arrives once this thread's products are done
+  } else if (warp == 18) {
+    // ======================= M4: D^T = V'^T K =======================
+    constexpr uint32_t id4 = umma::idesc_bf16(128, K, 0, 1);
+    for_chunks(nothing, [&](const LaItem &, int, int, int, int n) {
+      const int st = n % kStages;
+      const uint64_t kt = umma::sdesc_sw128(sbase + st * Lay::stage + Lay::k_off, Lay::panel, 1024);
+      if (!wait(&ms.full[st], (uint32_t)((n / kStages) & 1))) return false;
+      if (n > 0 && !wait(&ms.d_free, (uint32_t)((n - 1) & 1))) return false;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {   // 32 tokens: two steps of 16, three terms
+        const int buf = b & 1;
+        if (!wait(&ms.vp_rdy[buf], (uint32_t)(b >> 1))) return false;   // two phases per chunk: 0 and 1
+        if (umma::elect_one()) {
+#pragma unroll
+          for (int x = 0; x < 6; ++x)
+            umma::mma_f16_ts(tmem + kTmD, tmem + kTmVp + buf * kTmVpBuf + x * 8,
+                             umma::desc_add(kt, (2 * b + (x & 1)) * 2048), id4, b > 0 || x > 0);
+          umma::commit(&ms.vp_free[buf]);
+          if (b == 3) {
+            umma::commit(&ms.d_rdy);
+            umma::commit(&ms.empty[st]);
+            if constexpr (AGG) umma::commit(&ms.empty_v[st]);
+          }
+        }
+        __syncwarp();
+      }
+      return true;
+    }, nothing);
+    if (umma::elect_one()) umma::commit(&ms.bar_exit);
+  } else if (warp == 19) {
+    // ======================= output =======================
+    if constexpr (!AGG) {
+      for_chunks(nothing, [&](const LaItem &it, int h, int c, int, int n) {
+        const int st = n % kStages;
+        if (!wait(&ms.o_st[st], (uint32_t)((n / kStages) & 1))) return false;
+        const unsigned char *tile = sm + st * Lay::stage + Lay::v_off;
+        const int t0 = it.t0 + c * kLaChunk, L = min(kLaChunk, it.len - c * kLaChunk);
+        if (L == kLaChunk || !p.cu) {   // a partial chunk of an unpacked sequence ends at T, where the map ends
+          if (umma::elect_one()) {
+#pragma unroll
+            for (int x = 0; x < V / 64; ++x) umma::tma_store_4d(&maps.o, tile + x * Lay::panel, x * 64, h, t0, it.b);
+            umma::bulk_commit();
+            umma::bulk_wait_read();
+          }
+        } else {                        // the rows after it are the next packed sequence's
+          __nv_bfloat16 *dst = p.o + (((long long)it.b * p.T + t0) * p.H + h) * V;
+          for (int x = lane; x < L * (V / 8); x += 32) {
+            const int i = x / (V / 8), j = x % (V / 8);
+            *reinterpret_cast<uint4 *>(dst + (long long)i * p.H * V + j * 8) =
+                *reinterpret_cast<const uint4 *>(tile + (j >> 3) * Lay::panel + umma::sw128_chunk(i, j & 7));
+          }
+        }
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&ms.empty_v[st]);
+        return true;
+      }, nothing);
+    }
+  } else if (warp < 4) {
+    // ======================= P =======================
+    umma::regs_dec<kLaRegsP>();
+    if constexpr (!AGG) {
+      for_chunks(nothing, [&](const LaItem &, int, int, int, int n) {
+        const int st = (int)(n % kStages);
+        if (!wait(&ms.full[st], (uint32_t)((n / kStages) & 1))) return false;
+        const LaGate &g = gates[st];
+        const bool weak = g.G[kLaChunk - 1] >= kLaRowLog2;   // so are all sums of the chunk, for decays <= 1
+        const float Gi = g.G[row], Gr = Gi - fmaxf(Gi, kLaRowLog2);   // G_i - R_i
+        if (!wait(&ms.p_raw, (uint32_t)(n & 1))) return false;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+          if (c <= warp) {
+            float x[32];
+            umma::tmem_ld32(tmem + kTmP + lane_base + c * 32, x);
+            umma::tmem_ld_wait();
+            if (weak || c < warp) {
+              // exp(G_i - R_i - G_j) as the decay from j to its block's end and one factor of the block
+              const float f = ex2_approx(Gr - g.G[32 * c + 31]);
+              const float2 f2 = make_float2(f, f);
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 cf = *reinterpret_cast<const float4 *>(&g.cf[32 * c + j]);
+                const float2 a = __fmul2_rn(make_float2(x[j], x[j + 1]), __fmul2_rn(make_float2(cf.x, cf.y), f2));
+                const float2 b = __fmul2_rn(make_float2(x[j + 2], x[j + 3]), __fmul2_rn(make_float2(cf.z, cf.w), f2));
+                x[j] = a.x; x[j + 1] = a.y; x[j + 2] = b.x; x[j + 3] = b.y;
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] *= ex2_approx(Gr - g.G[32 * c + j]);
+            }
+            if (c == warp) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pk[j] = 0u;
+          }
+          umma::tmem_st16(tmem + kTmP + lane_base + c * 16, pk);
+        }
+        umma::tmem_st_wait();
+        arrive(&ms.p_rdy);
+        return true;
+      }, nothing);
+    }
+  } else if (warp < 8) {
+    // ======================= V' =======================
+    umma::regs_dec<kLaRegsV>();
+    for_chunks(nothing, [&](const LaItem &it, int, int c, int, int n) {
+      const int st = (int)(n % kStages);
+      if (!wait(&ms.full[st], (uint32_t)((n / kStages) & 1)) || !wait(&ms.full_v[st], (uint32_t)((n / kStages) & 1)))
+        return false;
+      unsigned char *kt = sm + st * Lay::stage + Lay::k_off, *vt = sm + st * Lay::stage + Lay::v_off;
+      const int L = min(kLaChunk, it.len - c * kLaChunk);
+      if (L < kLaChunk) {
+        // k and v rows past the sequence hold the next packed sequence: their factors are zero, but
+        // zero times an inf or NaN there would not be
+        for (int x = tid - 128; x < (kLaChunk - L) * 8; x += 128) {
+          const uint32_t off = (uint32_t)(L * 128 + x * 16);
+#pragma unroll
+          for (int y = 0; y < K / 64; ++y) *reinterpret_cast<uint4 *>(kt + y * Lay::panel + off) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int y = 0; y < V / 64; ++y) *reinterpret_cast<uint4 *>(vt + y * Lay::panel + off) = make_uint4(0, 0, 0, 0);
+        }
+        umma::fence_proxy_async_smem();
+        umma::named_bar(1, 128);
+      }
+      if constexpr (!AGG) arrive(&ms.v_rdy[st]);
+      const LaGate &g = gates[st];
+      // 8 x 8 blocks of the tile, transposed: matrix i of a load is channels 8 (i % 2), tokens 8 (i / 2) of
+      // this warp's 16 channels x 16 tokens; lane l names token l % 8 of matrix l / 8
+      const int ch0 = (warp & 3) * 32 + ((lane >> 3) & 1) * 8;
+      const uint32_t src = umma::smem_u32(vt) + (ch0 >> 6) * Lay::panel + ((lane >> 4) * 8 + (lane & 7)) * 128;
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {
+        const int buf = b & 1;
+        // M4 has read the buffer's last content (two phases per chunk: the one before this is b / 2 - 1)
+        if ((n > 0 || b >= 2) && !wait(&ms.vp_free[buf], (uint32_t)((b >> 1) ^ 1))) return false;
+        if ((warp & 3) * 32 < V) {
+          const float bf = g.bf[b];
+          float2 w[4];   // factors of tokens 8 m + 2 (l % 4) and the next
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            w[m] = __fmul2_rn(*reinterpret_cast<const float2 *>(&g.cf[32 * b + 8 * m + 2 * (lane & 3)]), make_float2(bf, bf));
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {   // 16 channels each
+            uint32_t raw[8], t0[8], t1[8], t2[8];
+            const uint32_t c16 = (uint32_t)(((((ch0 & 63) >> 3) + 2 * hh) ^ (lane & 7)) << 4);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              umma::ldmatrix_x4_trans(src + (32 * b + 16 * i) * 128 + c16, raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
+            const float2 minus = make_float2(-1.f, -1.f);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {   // token pairs 8 (r / 2) of channels 8 (r % 2)
+              float2 x = __fmul2_rn(make_float2(__uint_as_float(raw[r] << 16), __uint_as_float(raw[r] & 0xFFFF0000u)), w[r >> 1]);
+              t0[r] = pack_bf16(x.x, x.y);
+              x = __ffma2_rn(make_float2(__uint_as_float(t0[r] << 16), __uint_as_float(t0[r] & 0xFFFF0000u)), minus, x);
+              t1[r] = pack_bf16(x.x, x.y);
+              x = __ffma2_rn(make_float2(__uint_as_float(t1[r] << 16), __uint_as_float(t1[r] & 0xFFFF0000u)), minus, x);
+              t2[r] = pack_bf16(x.x, x.y);
+            }
+            const uint32_t dst = tmem + kTmVp + buf * kTmVpBuf + lane_base + ((uint32_t)(hh * 16) << 16);
+            umma::tmem_st_16x128b_x4(dst, t0);
+            umma::tmem_st_16x128b_x4(dst + 16, t1);
+            umma::tmem_st_16x128b_x4(dst + 32, t2);
+          }
+          umma::tmem_st_wait();
+        }
+        arrive(&ms.vp_rdy[buf]);
+      }
+      return true;
+    }, nothing);
+  } else if (warp < 16) {
+    // ======================= state and output =======================
+    umma::regs_inc<kLaRegsState>();
+    constexpr int KH = K / 2, VH = V / 2;      // this warpgroup's columns of S^T and of O
+    const int half = (warp - 8) >> 2;
+    const bool has_v = (warp & 3) * 32 < V;    // lanes are value columns of S^T, token rows of O
+    float S[KH];
+    float seg_decay = 1.f;
+    auto write_s = [&] {                       // bf16 copy of S^T, the operand of M2
+      if constexpr (!AGG) {
+        if (has_v) {
+#pragma unroll
+          for (int x = 0; x < KH / 8; ++x) {
+            const int k = half * KH + x * 8;
+            *reinterpret_cast<uint4 *>(sm + Lay::s_off + (k >> 6) * Lay::s_panel + umma::sw128_chunk(row, (k & 63) >> 3)) =
+                make_uint4(pack_bf16(S[8 * x], S[8 * x + 1]), pack_bf16(S[8 * x + 2], S[8 * x + 3]),
+                           pack_bf16(S[8 * x + 4], S[8 * x + 5]), pack_bf16(S[8 * x + 6], S[8 * x + 7]));
+          }
+        }
+        umma::fence_proxy_async_smem();
+        arrive(&ms.s_rdy);
+      }
+    };
+    auto seg_block = [&](int slot, int h) { return p.seg_state + ((long long)slot * p.H + h) * (K * V); };
+    for_chunks(
+        [&](const LaItem &it, int h, int nch) {
+          if (AGG || (it.seg == 0 && !p.init) || !has_v) {
+#pragma unroll
+            for (int j = 0; j < KH; ++j) S[j] = 0.f;
+          } else if (it.seg == 0) {
+            la_state_load<K, V>(p, it.seq, h, row, half * KH, S);
+          } else {
+            const float *src = seg_block(it.slot - 1, h);
+#pragma unroll
+            for (int j = 0; j < KH / 4; ++j) {
+              const float4 f = *reinterpret_cast<const float4 *>(src + la_seg_index<K, V>(half, row, j));
+              S[4 * j] = f.x; S[4 * j + 1] = f.y; S[4 * j + 2] = f.z; S[4 * j + 3] = f.w;
+            }
+          }
+          seg_decay = 1.f;
+          if (nch > 0) write_s();   // M2 of the item before has read its copy (s_free)
+          return true;
+        },
+        [&](const LaItem &it, int h, int c, int nch, int n) {
+          const int st = (int)(n % kStages);
+          const uint32_t ph = (uint32_t)(n & 1);
+          if (!wait(&ms.full[st], (uint32_t)((n / kStages) & 1))) return false;
+          const float gamma = gates[st].gamma;
+          float f = 0.f;   // scale exp(R_i) of this thread's token row
+          if constexpr (!AGG) f = p.scale * ex2_approx(fmaxf(gates[st].G[row], kLaRowLog2));
+          arrive(&ms.empty[st]);   // the factors have been read
+          if (!wait(&ms.d_rdy, ph)) return false;
+          if (has_v) {
+#pragma unroll
+            for (int x = 0; x < KH; x += 16) {
+              float y[16];
+              umma::tmem_ld16(tmem + kTmD + lane_base + half * KH + x, y);
+              umma::tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                const float2 a = __ffma2_rn(make_float2(gamma, gamma), make_float2(S[x + j], S[x + j + 1]), make_float2(y[j], y[j + 1]));
+                S[x + j] = a.x;
+                S[x + j + 1] = a.y;
+              }
+            }
+          }
+          arrive(&ms.d_free);
+          if constexpr (AGG) seg_decay *= gamma;
+          if constexpr (!AGG) {
+            if (!wait(&ms.s_free, ph)) return false;   // M2 has read the copy of S
+          }
+          if (c + 1 < nch) write_s();
+          if constexpr (!AGG) {
+            if (!wait(&ms.o_done, ph)) return false;
+            // o in bf16 over the chunk's v: M3 has read it, and so have the V' warps (d_rdy)
+            unsigned char *tile = sm + st * Lay::stage + Lay::v_off;
+#pragma unroll 1
+            for (int x = 0; x < VH; x += 32) {
+              float y[32];
+              umma::tmem_ld32(tmem + kTmO + lane_base + half * VH + x, y);
+              umma::tmem_ld_wait();
+              if (x + 32 >= VH) arrive(&ms.o_free);
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float2 a = __fmul2_rn(make_float2(y[j], y[j + 1]), make_float2(f, f));
+                y[j] = a.x;
+                y[j + 1] = a.y;
+              }
+              const int col = half * VH + x;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4 *>(tile + (col >> 6) * Lay::panel + umma::sw128_chunk(row, ((col & 63) >> 3) + j)) =
+                    make_uint4(pack_bf16(y[8 * j], y[8 * j + 1]), pack_bf16(y[8 * j + 2], y[8 * j + 3]),
+                               pack_bf16(y[8 * j + 4], y[8 * j + 5]), pack_bf16(y[8 * j + 6], y[8 * j + 7]));
+            }
+            umma::fence_proxy_async_smem();
+            arrive(&ms.o_st[st]);
+          }
+          return true;
+        },
+        [&](const LaItem &it, int h, int) {
+          if (!has_v) return true;
+          if constexpr (AGG) {
+            float *dst = seg_block(it.slot, h);
+#pragma unroll
+            for (int j = 0; j < KH / 4; ++j)
+              *reinterpret_cast<float4 *>(dst + la_seg_index<K, V>(half, row, j)) =
+                  make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+            if (tid == 8 * 32) p.seg_decay[(long long)it.slot * p.H + h] = seg_decay;
+          } else if (it.seg == it.n_seg - 1 && p.final_state) {
+            la_state_store<K, V>(p, it.seq, h, row, half * KH, S);
+          }
+          return true;
+        });
+  }
+
+  // no product of this CTA may be in flight past this point
+  if (warp == 17 || warp == 18) umma::mbar_wait_bounded(&ms.bar_exit, 0, kLaWaitLimit);
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  if (tid == 0 && ms.err) atomicExch(p.dev_status, kDevWaitTimeout);
+  if (warp == 0) umma::tmem_dealloc(tmem, kLaTmemCols);
+}
+
+// Start states of the segments: chains, over the segments of a sequence, what each segment adds.
+// One thread per four state values; segment g's block is read and then holds the start of g + 1.
+template <int K, int V>
+__global__ void __launch_bounds__(256) la_combine_kernel(const LaProblem p) {
+  pdl_wait();
+  if (p.flag && *p.flag != kDevOk) return;
+  const int s = blockIdx.x / p.H, h = blockIdx.x % p.H;
+  const int slot0 = p.cu ? p.slot0[s] : s * p.n_seg;
+  const int n = p.cu ? p.slot0[s + 1] - slot0 : p.n_seg;
+  const int x = blockIdx.y * 256 + threadIdx.x;             // float4 index of the block
+  const int j = x / (2 * V), half = (x / V) & 1, v = x % V;
+  if (n < 2) return;
+  float S[4] = {0.f, 0.f, 0.f, 0.f};
+  if (p.init) {
+    const long long base = ((long long)s * p.H + h) * (K * V);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int k = half * (K / 2) + 4 * j + e;
+      const long long i = base + ((p.flags & kStateKV) ? k * V + v : v * K + k);
+      S[e] = (p.flags & kStateBf16) ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.init)[i])
+                                    : static_cast<const float *>(p.init)[i];
+    }
+  }
+  for (int g = 0; g + 1 < n; ++g) {
+    const long long block = (long long)(slot0 + g) * p.H + h;
+    float4 *at = reinterpret_cast<float4 *>(p.seg_state + block * (K * V)) + x;
+    const float d = p.seg_decay[block];
+    const float4 f = *at;
+    S[0] = fmaf(d, S[0], f.x);
+    S[1] = fmaf(d, S[1], f.y);
+    S[2] = fmaf(d, S[2], f.z);
+    S[3] = fmaf(d, S[3], f.w);
+    *at = make_float4(S[0], S[1], S[2], S[3]);
+  }
+}
+// Varlen schedule: checks cu_seqlens, cuts the sequences into segments of seg_chunks chunks and lists
+// them longest first (counting sort; very long segments share bins, which only makes the order
+// approximate). One CTA.
+constexpr int kLaSchedThreads = 1024, kLaSchedBins = 2048;
+
+__global__ void __launch_bounds__(kLaSchedThreads) la_schedule_kernel(const LaProblem p) {
+  __shared__ int s_bad;
+  __shared__ int s_scan[kLaSchedThreads];
+  __shared__ int s_bins[kLaSchedBins];
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, N = p.N;
+  const int32_t *cu = p.cu;
+  if (tid == 0) s_bad = (cu[0] != 0 || cu[N] != p.T) ? 1 : 0;
+  for (int b = tid; b < kLaSchedBins; b += kLaSchedThreads) s_bins[b] = 0;
+  __syncthreads();
+  for (int i = tid; i < N; i += kLaSchedThreads)
+    if (cu[i + 1] < cu[i]) atomicOr(&s_bad, 1);
+  __syncthreads();
+  if (s_bad) {
+    if (tid == 0) {
+      *p.flag = kDevBadCuSeqlens;
+      atomicExch(p.dev_status, kDevBadCuSeqlens);
+    }
+    return;
+  }
+  if (tid == 0) *p.flag = kDevOk;
+  const int longest = min(p.seg_chunks, (p.T + kLaChunk - 1) / kLaChunk);
+  const int per_bin = longest / kLaSchedBins + 1;   // chunk counts per bin; bins in descending order
+  auto bin_of = [&](int chunks) { return (longest - chunks) / per_bin; };
+  int carry = 0;
+  for (int base = 0; base < N; base += kLaSchedThreads) {
+    const int i = base + tid;
+    int n = 0;
+    if (i < N) {
+      const int nc = (cu[i + 1] - cu[i] + kLaChunk - 1) / kLaChunk;
+      n = max(1, (nc + p.seg_chunks - 1) / p.seg_chunks);
+      if (n > 1) atomicAdd(&s_bins[0], n - 1);
+      atomicAdd(&s_bins[bin_of(nc - (n - 1) * p.seg_chunks)], 1);
+    }
+    s_scan[tid] = n;
+    __syncthreads();
+    for (int off = 1; off < kLaSchedThreads; off <<= 1) {
+      const int x = (tid >= off) ? s_scan[tid - off] : 0;
+      __syncthreads();
+      s_scan[tid] += x;
+      __syncthreads();
+    }
+    if (i < N) p.slot0[i] = carry + s_scan[tid] - n;
+    carry += s_scan[kLaSchedThreads - 1];
+    __syncthreads();
+  }
+  if (tid == 0) {
+    p.slot0[N] = carry;
+    *p.n_items = carry;
+  }
+  // exclusive scan of the bins, two per thread
+  const int x0 = s_bins[2 * tid], x1 = s_bins[2 * tid + 1];
+  s_scan[tid] = x0 + x1;
+  __syncthreads();
+  for (int off = 1; off < kLaSchedThreads; off <<= 1) {
+    const int x = (tid >= off) ? s_scan[tid - off] : 0;
+    __syncthreads();
+    s_scan[tid] += x;
+    __syncthreads();
+  }
+  s_bins[2 * tid] = s_scan[tid] - x0 - x1;
+  s_bins[2 * tid + 1] = s_scan[tid] - x1;
+  __syncthreads();
+  for (int i = tid; i < N; i += kLaSchedThreads) {
+    const int t0 = cu[i], len = cu[i + 1] - t0;
+    const int nc = (len + kLaChunk - 1) / kLaChunk, n = max(1, (nc + p.seg_chunks - 1) / p.seg_chunks);
+    const int seg_len = p.seg_chunks * kLaChunk;
+    const int first = n > 1 ? atomicAdd(&s_bins[0], n - 1) : 0;
+    for (int g = 0; g < n; ++g) {
+      LaItem it;
+      it.seq = i;
+      it.b = 0;
+      it.seg = g;
+      it.n_seg = n;
+      it.slot = p.slot0[i] + g;
+      it.t0 = n > 1 ? t0 + g * seg_len : t0;
+      it.len = g < n - 1 ? seg_len : len - (it.t0 - t0);
+      it.pad = 0;
+      const int pos = g < n - 1 ? first + g : atomicAdd(&s_bins[bin_of(nc - (n - 1) * p.seg_chunks)], 1);
+      p.items[pos] = it;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------- host
+
+// How a call is cut: chunks per segment, segments per sequence (fixed length) and the slots that
+// the workspace holds.
+struct LaPlan {
+  int seg_chunks, n_seg;
+  long long slots;
+  bool segments;   // whether any sequence may have more than one segment
+};
+
+static LaPlan la_plan(int T, int H, int N, bool varlen) {
+  LaPlan r;
+  const int nc = std::max(1, (int)(((long long)T + kLaChunk - 1) / kLaChunk));
+  r.seg_chunks = nc;
+  r.n_seg = 1;
+  r.segments = false;
+  r.slots = varlen ? (long long)T / ((long long)r.seg_chunks * kLaChunk) + 2ll * N : (long long)N * r.n_seg;
+  return r;
+}
+
+struct LaScratch {
+  size_t flag, n_items, slot0, items, decay, state, total;
+};
+static LaScratch la_scratch(const LaPlan &pl, int H, int K, int V, int N, bool varlen) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  LaScratch s = {};
+  size_t off = 0;
+  if (varlen) {
+    s.flag = off;
+    s.n_items = off + 4;
+    off = up(off + 8);
+    s.slot0 = off;
+    off = up(off + 4 * ((size_t)N + 1));
+    s.items = off;
+    off = up(off + sizeof(LaItem) * (size_t)pl.slots);
+  }
+  if (pl.segments) {
+    s.decay = off;
+    off = up(off + 4 * (size_t)pl.slots * H);
+    s.state = off;
+    off = up(off + 4 * (size_t)pl.slots * H * K * V);
+  }
+  s.total = off;
+  return s;
+}
+
+template <int K, int V, bool AGG>
+static cudaError_t launch_la_t(const LaProblem &p, const LaMaps &maps, long long items, cudaStream_t stream, bool overlap) {
+  static PerDeviceOnce attr;
+  constexpr int smem = (int)LaLayout<K, V, AGG>::bytes;
+  cudaError_t e = attr([&](int) {
+    return cudaFuncSetAttribute(la_kernel<K, V, AGG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  if (e != cudaSuccess) return e;
+  const int sms = device_sm_count();
+  const long long grid = std::min(items * p.H, (long long)(sms > 0 ? sms : 1));
+  return launch_kernel(la_kernel<K, V, AGG>, dim3((unsigned)grid), dim3(kLaThreads), smem, stream, overlap, p, maps);
+}
+
+template <int K, int V>
+static cudaError_t launch_la(const LaProblem &p, const LaMaps &maps, const LaPlan &pl, cudaStream_t s) {
+  const long long items = p.cu ? pl.slots : (long long)p.N * pl.n_seg;
+  bool overlap = p.cu != nullptr;
+  if (p.cu) {
+    const cudaError_t e = launch_kernel(la_schedule_kernel, dim3(1), dim3(kLaSchedThreads), 0, s, false, p);
+    if (e != cudaSuccess) return e;
+  }
+  if (pl.segments) {
+    cudaError_t e = launch_la_t<K, V, true>(p, maps, items, s, overlap);
+    if (e == cudaSuccess)
+      e = launch_kernel(la_combine_kernel<K, V>, dim3((unsigned)(p.N * p.H), K * V / 1024), dim3(256), 0, s, false, p);
+    if (e != cudaSuccess) return e;
+    overlap = false;
+  }
+  return launch_la_t<K, V, false>(p, maps, items, s, overlap);
+}
+
+static bool la_sizes_ok(int B, int T, int Hk, int H, int K, int V, int N) {
+  return B >= 1 && T >= 0 && Hk >= 1 && H >= 1 && H % Hk == 0 && K >= 1 && V >= 1 && N >= 0;
+}
+
+}  // namespace kda
+
+extern "C" {
+
+size_t kda_la_workspace_size(int B, int T, int H, int K, int V, int num_seqs, int varlen) {
+  using namespace kda;
+  if (!la_sizes_ok(B, T, 1, H, K, V, num_seqs)) return 0;
+  return la_scratch(la_plan(T, H, num_seqs, varlen != 0), H, K, V, num_seqs, varlen != 0).total;
+}
+
+kda_status_t kda_la_fwd(const void *q, const void *k, const void *v, const float *log_decay, float scale,
+                        const void *initial_state, void *final_state, const int32_t *cu_seqlens, int B, int T, int Hk,
+                        int H, int K, int V, int num_seqs, const kda_la_strides_t *strides, uint32_t flags, void *o,
+                        void *workspace, size_t workspace_bytes, kda_stream_t stream) {
+  using namespace kda;
+  if (flags & ~(kLaTokenDecay | kStateBf16 | kStateKV)) return KDA_ERR_INVALID_ARG;
+  if (!la_sizes_ok(B, T, Hk, H, K, V, num_seqs)) return KDA_ERR_INVALID_ARG;
+  if (!log_decay || (T > 0 && (!q || !k || !v || !o))) return KDA_ERR_INVALID_ARG;
+  if ((K != 64 && K != 128) || (V != 64 && V != 128)) return KDA_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale)) return KDA_ERR_INVALID_ARG;
+  if (cu_seqlens ? (B != 1 || !aligned(cu_seqlens, 4)) : num_seqs != B) return KDA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(log_decay, 4) ||
+      !aligned(initial_state, 16) || !aligned(final_state, 16))
+    return KDA_ERR_INVALID_ARG;
+  const int64_t contiguous[3][3] = {{(int64_t)T * Hk * K, (int64_t)Hk * K, K},
+                                    {(int64_t)T * H * V, (int64_t)H * V, V},
+                                    {(int64_t)T * H, H, 1}};
+  const int64_t *sq = strides ? strides->q : contiguous[0], *sk = strides ? strides->k : contiguous[0];
+  const int64_t *sv = strides ? strides->v : contiguous[1], *sd = strides ? strides->log_decay : contiguous[2];
+  const int64_t extent[3] = {B, T, 0};
+  for (int i = 0; i < 3; ++i) {
+    const int64_t *s3[3] = {sq, sk, sv};
+    for (int x = 0; x < 3; ++x) {
+      const int64_t n = i < 2 ? extent[i] : (x == 2 ? H : Hk);
+      if (n > 1 && (s3[x][i] < 0 || s3[x][i] % 8 != 0 || s3[x][i] >= (int64_t)1 << 39)) return KDA_ERR_INVALID_ARG;
+    }
+  }
+  if ((double)B * T * H * std::max(K, V) > 9.0e15 || (double)num_seqs * H > 2.0e9) return KDA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return KDA_OK;
+  const bool varlen = cu_seqlens != nullptr;
+  const LaPlan pl = la_plan(T, H, num_seqs, varlen);
+  const LaScratch L = la_scratch(pl, H, K, V, num_seqs, varlen);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  void *ws = workspace;
+  if (L.total > 0) {
+    if (workspace) {
+      if (workspace_bytes < L.total || !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;
+    } else if (cudaMallocAsync(&ws, L.total, s) != cudaSuccess) {
+      cudaGetLastError();
+      return KDA_ERR_WORKSPACE;
+    }
+  }
+  LaProblem p;
+  std::memset(&p, 0, sizeof p);
+  char *base = static_cast<char *>(ws);
+  p.decay = log_decay;
+  for (int i = 0; i < 3; ++i) p.ds[i] = sd[i];
+  p.init = initial_state;
+  p.final_state = final_state;
+  p.cu = cu_seqlens;
+  p.o = static_cast<__nv_bfloat16 *>(o);
+  if (varlen) {
+    p.flag = reinterpret_cast<int32_t *>(base + L.flag);
+    p.n_items = reinterpret_cast<int32_t *>(base + L.n_items);
+    p.slot0 = reinterpret_cast<int32_t *>(base + L.slot0);
+    p.items = reinterpret_cast<LaItem *>(base + L.items);
+  }
+  if (pl.segments) {
+    p.seg_decay = reinterpret_cast<float *>(base + L.decay);
+    p.seg_state = reinterpret_cast<float *>(base + L.state);
+  }
+  p.scale = scale;
+  p.B = B; p.T = T; p.Hk = Hk; p.H = H; p.N = num_seqs;
+  p.seg_chunks = pl.seg_chunks;
+  p.n_seg = pl.n_seg;
+  p.flags = flags;
+  p.dev_status = device_status_address();
+  kda_status_t st = p.dev_status ? KDA_OK : KDA_ERR_CUDA;
+  LaMaps maps;
+  std::memset(&maps, 0, sizeof maps);
+  if (st == KDA_OK && T > 0) {
+    auto encode = [&](CUtensorMap *m, const void *ptr, int D, int heads, const int64_t *e) {
+      const long long bytes[3] = {(long long)e[2] * 2, (long long)e[1] * 2, (long long)e[0] * 2};
+      return encode_swizzled_token_map(m, ptr, D, heads, T, B, bytes, kLaChunk);
+    };
+    if (!encode(&maps.q, q, K, Hk, sq) || !encode(&maps.k, k, K, Hk, sk) || !encode(&maps.v, v, V, H, sv) ||
+        !encode(&maps.o, o, V, H, contiguous[1]))
+      st = KDA_ERR_CUDA;
+  }
+  if (st == KDA_OK) {
+    NvtxRange r("kda la forward");
+    const cudaError_t e = K == 128 ? (V == 128 ? launch_la<128, 128>(p, maps, pl, s) : launch_la<128, 64>(p, maps, pl, s))
+                                   : (V == 128 ? launch_la<64, 128>(p, maps, pl, s) : launch_la<64, 64>(p, maps, pl, s));
+    if (e != cudaSuccess) st = KDA_ERR_CUDA;
+  }
+  if (L.total > 0 && !workspace) cudaFreeAsync(ws, s);
+  return st;
+}
+
+}  // extern "C"

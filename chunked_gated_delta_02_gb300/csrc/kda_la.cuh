@@ -1,0 +1,47 @@
+// Linear attention with one decay per head, chunked form: what the kernels and the host share.
+#pragma once
+
+#include "kda_common.cuh"
+
+namespace kda {
+
+constexpr int kLaChunk = 128;   // tokens per chunk: one 128-row tensor-core tile
+
+// A run of chunks of one sequence that one CTA takes for one head.
+struct LaItem {
+  int seq;
+  int t0, len;        // tokens [t0, t0 + len) of batch row b
+  int b;
+  int slot;           // index of its segment among all segments
+  int seg, n_seg;     // segment of the sequence, number of them
+  int pad;
+};
+
+struct LaProblem {
+  const float *decay;            // log decay, [H] or per token (kLaTokenDecay)
+  long long ds[3];               // strides of the per-token log decay: batch row, token, head
+  const void *init;              // [N,H,V,K] or [N,H,K,V], fp32 or bf16, or null
+  void *final_state;             // the same, or null
+  const int32_t *cu;             // [N+1] or null
+  __nv_bfloat16 *o;              // [B,T,H,V]
+  // Segments (n_seg > 1): slot s of head h holds at seg_state + (s H + h) K V first the state that
+  // the segment adds when started from zero, after the combine the start state of segment s + 1;
+  // seg_decay[s H + h] is the product of its decays.
+  float *seg_state;
+  float *seg_decay;
+  LaItem *items;                 // varlen work list, longest first (schedule kernel)
+  int32_t *n_items;
+  int32_t *slot0;                // [N] first slot of each sequence (varlen)
+  int32_t *flag;                 // per-call data-error flag (varlen) or null
+  int *dev_status;
+  float scale;
+  int B, T, Hk, H, N;
+  int seg_chunks, n_seg;         // chunks per segment; segments per sequence (fixed length)
+  uint32_t flags;
+};
+
+struct LaMaps {
+  CUtensorMap q, k, v, o;
+};
+
+}  // namespace kda

@@ -1,0 +1,422 @@
+// Single-token recurrences over a pool of states (decoding): one token of the KDA recurrence, or
+// of linear attention with one decay per head, for each of N requests.
+//
+// Per request n and head h, with the state S (K x V) of pool row state_indices[n]:
+//   KDA:               s = Diag(alpha) S;  u = beta (v - s^T khat);  S' = s + khat u^T
+//   linear attention:  S' = exp(a) S + k v^T
+//   o = scale S'^T q   (KDA: qhat; alpha, khat, qhat and beta as in kda_fwd)
+//
+// For KDA the output needs no second pass over S': o = scale (s^T qhat + (qhat . khat) u), so both
+// products s^T khat and s^T qhat are formed in one sweep and S' is written from registers.
+//
+// Bound: the state is read and written once, 128 KiB per request and head at K = V = 128 in fp32,
+// against about 1 KiB of token data and 7 K V operations: memory bandwidth. A CTA of 128 threads
+// takes a 16 KiB tile of one state (whole rows of the contiguous dimension's 128 bytes per 8
+// lanes), and issues all loads of the tile before it computes anything: the gate, the norms and
+// the block reduction run while the tile is in flight. Small batches (N H < SM count) still give
+// V / 32 CTAs per state.
+#include <cmath>
+#include <cstring>
+
+#include "../../include/kda.h"
+#include "kda_common.cuh"
+#include "kda_host.cuh"
+
+namespace kda {
+
+constexpr int kStepThreads = 128;
+constexpr int kStepWarps = kStepThreads / 32;
+
+struct StepArgs {
+  const __nv_bfloat16 *q, *k, *v;
+  const void *g;               // KDA: bf16 gate; linear attention: fp32 log decay per token, or per head
+  const void *beta;            // KDA: logits, bf16 or fp32
+  const float *A_log, *dt_bias;
+  void *state;                 // [num_states, H, V, K] or [num_states, H, K, V]
+  const int32_t *idx;          // [N] pool rows, or null: row n
+  __nv_bfloat16 *o;            // [N, H, V]
+  int *dev_status;
+  long long num_states;
+  long long qs[2], ks[2], vs[2], gs[2], bs[2];   // strides in elements: request, head
+  float lb, scale;
+  int N, H, group, V;          // group: value heads per query / key head
+  uint32_t flags;
+};
+
+// 16 bytes of state: 4 fp32 or 8 bf16 values.
+template <typename ST> struct StateVec;
+template <> struct StateVec<float> {
+  static constexpr int n = 4;
+  __device__ static __forceinline__ void unpack(const uint4 &r, float (&x)[4]) {
+    x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y);
+    x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
+  }
+  __device__ static __forceinline__ uint4 pack(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
+};
+template <> struct StateVec<__nv_bfloat16> {
+  static constexpr int n = 8;
+  __device__ static __forceinline__ void unpack(const uint4 &r, float (&x)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  // the one rounding of a bf16 state per token, to nearest even
+  __device__ static __forceinline__ uint4 pack(const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+template <int N>
+__device__ __forceinline__ void load_shared(const float *src, float (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const float4 f = *reinterpret_cast<const float4 *>(src + i);
+    x[i] = f.x; x[i + 1] = f.y; x[i + 2] = f.z; x[i + 3] = f.w;
+  }
+}
+
+// Tile of one CTA: R rows x CB columns of the stored matrix, CB along the contiguous dimension.
+//   [V, K] layout: rows are value columns v, a row holds all K channels (CB = K);
+//   [K, V] layout: rows are all K channels, CB value columns (128 bytes).
+// 8 lanes cover 128 bytes of a row, a warp 4 rows, the CTA 16 rows per pass.
+template <int K, typename ST, bool KV>
+struct StepTile {
+  static constexpr int vec = StateVec<ST>::n;
+  static constexpr int span = 8 * vec;                                   // values of 8 lanes: 128 bytes
+  static constexpr int cols = KV ? span : K;
+  static constexpr int per_row = cols / span;                            // 16-byte loads per lane and row
+  static constexpr int rows = KV ? K : (per_row == 4 ? 32 : 64);
+  static constexpr int passes = rows / (4 * kStepWarps);
+  static constexpr int slice = KV ? cols : rows;                         // value columns per CTA
+};
+
+template <bool KDA, int K, typename ST, bool KV>
+__global__ void __launch_bounds__(kStepThreads, 6) step_kernel(const StepArgs a) {
+  using T = StepTile<K, ST, KV>;
+  using Vec = StateVec<ST>;
+  constexpr int kVec = T::vec;
+  __shared__ __align__(16) float s_q[K], s_k[K], s_a[K], s_v[T::slice];
+  __shared__ float s_part[3][kStepWarps];
+  __shared__ float s_red[KV ? 2 : 1][KV ? kStepWarps : 1][T::slice];   // [K, V] layout: sums over the warps
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slices = a.V / T::slice;
+  const int v0 = (int)(blockIdx.x % slices) * T::slice;
+  const int nh = (int)(blockIdx.x / slices);
+  const int n = nh / a.H, h = nh % a.H;
+  __nv_bfloat16 *o = a.o + (long long)nh * a.V + v0;
+  const long long row = a.idx ? (long long)a.idx[n] : (long long)n;
+  if (row < 0 || row >= a.num_states) {   // a padding entry, or an index outside the pool: no state is touched
+    if (row >= a.num_states && tid == 0) atomicExch(a.dev_status, kDevBadStateIndex);
+    if (tid < T::slice) o[tid] = __float2bfloat16_rn(0.f);
+    return;
+  }
+  const int c = lane & 7, r = warp * 4 + (lane >> 3);
+  ST *tile = static_cast<ST *>(a.state) + (row * a.H + h) * (long long)K * a.V + (KV ? v0 : (long long)v0 * K);
+  const long long ld = KV ? a.V : K;
+
+  // ---- all of the tile's loads first
+  uint4 raw[T::passes][T::per_row];
+#pragma unroll
+  for (int p = 0; p < T::passes; ++p)
+#pragma unroll
+    for (int j = 0; j < T::per_row; ++j)
+      raw[p][j] = __ldcs(reinterpret_cast<const uint4 *>(tile + (p * 16 + r) * ld + j * T::span + c * kVec));
+
+  // ---- token data: channel tid of q, k and the decay; value column tid of the slice
+  float sums[3] = {0.f, 0.f, 0.f};   // |q|^2, |k|^2, q . k
+  if (tid < K) {
+    const int hk = h / a.group;
+    const float qv = __bfloat162float(a.q[n * a.qs[0] + hk * a.qs[1] + tid]);
+    const float kv = __bfloat162float(a.k[n * a.ks[0] + hk * a.ks[1] + tid]);
+    s_q[tid] = qv;
+    s_k[tid] = kv;
+    if constexpr (KDA) {
+      const bool per_head = a.flags & kGatePerHead;
+      const float g = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.g)[n * a.gs[0] + h * a.gs[1] + (per_head ? 0 : tid)]);
+      const float dt = a.dt_bias ? a.dt_bias[per_head ? h : h * K + tid] : 0.f;
+      s_a[tid] = ex2_approx(log2_decay(g, dt, ex2_approx(a.A_log[h] * kLog2e), a.lb * kLog2e));
+      sums[0] = qv * qv;
+      sums[1] = kv * kv;
+      sums[2] = qv * kv;
+    }
+  }
+  if (tid < T::slice) s_v[tid] = __bfloat162float(a.v[n * a.vs[0] + h * a.vs[1] + v0 + tid]);
+  float beta = 1.f, decay = 1.f;
+  if constexpr (KDA) {
+    const long long bi = n * a.bs[0] + h * a.bs[1];
+    beta = sigmoid_fast((a.flags & kBetaF32) ? static_cast<const float *>(a.beta)[bi]
+                                             : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.beta)[bi]));
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      sums[i] = warp_sum(sums[i]);
+      if (lane == 0) s_part[i][warp] = sums[i];
+    }
+  } else {
+    decay = ex2_approx(static_cast<const float *>(a.g)[(a.flags & kLaTokenDecay) ? n * a.gs[0] + h * a.gs[1] : h] * kLog2e);
+  }
+  __syncthreads();
+  float rq = 1.f, rk = 1.f, qk = 0.f;   // norm factors of q and k, and qhat . khat
+  if constexpr (KDA) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      sums[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kStepWarps; ++w) sums[i] += s_part[i][w];
+    }
+    rq = rsqrtf(sums[0] + kNormEps);
+    rk = rsqrtf(sums[1] + kNormEps);
+    qk = sums[2] * rq * rk;
+  }
+
+  if constexpr (!KV) {
+    // Rows are value columns: the products over k are sums over a lane's values and 8 lanes.
+#pragma unroll
+    for (int p = 0; p < T::passes; ++p) {
+      const int vi = p * 16 + r;
+      const float vv = s_v[vi];
+      float x[T::per_row][kVec];
+      float d1 = 0.f, d2 = 0.f;
+#pragma unroll
+      for (int j = 0; j < T::per_row; ++j) {
+        const int k0 = j * T::span + c * kVec;
+        float kk[kVec], qq[kVec];
+        load_shared(s_k + k0, kk);
+        load_shared(s_q + k0, qq);
+        Vec::unpack(raw[p][j], x[j]);
+        if constexpr (KDA) {
+          float aa[kVec];
+          load_shared(s_a + k0, aa);
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            x[j][e] *= aa[e];
+            d1 = fmaf(kk[e], x[j][e], d1);
+            d2 = fmaf(qq[e], x[j][e], d2);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            x[j][e] = fmaf(decay, x[j][e], kk[e] * vv);
+            d2 = fmaf(qq[e], x[j][e], d2);
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 1; m < 8; m <<= 1) {
+        if constexpr (KDA) d1 += __shfl_xor_sync(0xffffffffu, d1, m);
+        d2 += __shfl_xor_sync(0xffffffffu, d2, m);
+      }
+      float out = d2;
+      if constexpr (KDA) {
+        const float u = beta * (vv - rk * d1);
+        const float ku = rk * u;
+        out = fmaf(qk, u, rq * d2);
+#pragma unroll
+        for (int j = 0; j < T::per_row; ++j) {
+          float kk[kVec];
+          load_shared(s_k + j * T::span + c * kVec, kk);
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) x[j][e] = fmaf(ku, kk[e], x[j][e]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < T::per_row; ++j)
+        __stcs(reinterpret_cast<uint4 *>(tile + vi * ld + j * T::span + c * kVec), Vec::pack(x[j]));
+      if (c == 0) o[vi] = __float2bfloat16_rn(a.scale * out);
+    }
+  } else {
+    // Rows are channels k: the products over k are sums over a lane's rows, 4 lanes and the warps.
+    float d1[kVec], d2[kVec], vv[kVec];
+    load_shared(s_v + c * kVec, vv);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) d1[e] = d2[e] = 0.f;
+#pragma unroll
+    for (int p = 0; p < T::passes; ++p) {
+      const int k = p * 16 + r;
+      const float kk = s_k[k], qq = s_q[k];
+      float x[kVec];
+      Vec::unpack(raw[p][0], x);
+      if constexpr (KDA) {
+        const float aa = s_a[k];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          const float s = aa * x[e];
+          d1[e] = fmaf(kk, s, d1[e]);
+          d2[e] = fmaf(qq, s, d2[e]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          x[e] = fmaf(decay, x[e], kk * vv[e]);
+          d2[e] = fmaf(qq, x[e], d2[e]);
+        }
+        __stcs(reinterpret_cast<uint4 *>(tile + k * ld + c * kVec), Vec::pack(x));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+#pragma unroll
+      for (int m = 8; m < 32; m <<= 1) {
+        if constexpr (KDA) d1[e] += __shfl_xor_sync(0xffffffffu, d1[e], m);
+        d2[e] += __shfl_xor_sync(0xffffffffu, d2[e], m);
+      }
+      if (lane < 8) {
+        s_red[0][warp][c * kVec + e] = d2[e];
+        if constexpr (KDA) s_red[1][warp][c * kVec + e] = d1[e];
+      }
+    }
+    __syncthreads();
+    if constexpr (KDA) {
+      float u[kVec];
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kStepWarps; ++w) s += s_red[1][w][c * kVec + e];
+        u[e] = beta * (vv[e] - rk * s);
+      }
+#pragma unroll
+      for (int p = 0; p < T::passes; ++p) {
+        const int k = p * 16 + r;
+        const float ku = rk * s_k[k], aa = s_a[k];
+        float x[kVec];
+        Vec::unpack(raw[p][0], x);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) x[e] = fmaf(ku, u[e], aa * x[e]);
+        __stcs(reinterpret_cast<uint4 *>(tile + k * ld + c * kVec), Vec::pack(x));
+      }
+    }
+    if (tid < T::slice) {
+      float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kStepWarps; ++w) {
+        s2 += s_red[0][w][tid];
+        if constexpr (KDA) s1 += s_red[1][w][tid];
+      }
+      if constexpr (KDA) s2 = fmaf(qk, beta * (s_v[tid] - rk * s1), rq * s2);
+      o[tid] = __float2bfloat16_rn(a.scale * s2);
+    }
+  }
+}
+
+template <bool KDA, int K, typename ST, bool KV>
+static cudaError_t launch_step_t(const StepArgs &a, cudaStream_t stream) {
+  const long long grid = (long long)a.N * a.H * (a.V / StepTile<K, ST, KV>::slice);
+  return launch_kernel(step_kernel<KDA, K, ST, KV>, dim3((unsigned)grid), dim3(kStepThreads), 0, stream, false, a);
+}
+
+template <bool KDA>
+static cudaError_t launch_step(const StepArgs &a, int K, cudaStream_t stream) {
+  const bool bf16 = a.flags & kStateBf16, kv = a.flags & kStateKV;
+  if (K == 64) {
+    if (bf16) return kv ? launch_step_t<KDA, 64, __nv_bfloat16, true>(a, stream) : launch_step_t<KDA, 64, __nv_bfloat16, false>(a, stream);
+    return kv ? launch_step_t<KDA, 64, float, true>(a, stream) : launch_step_t<KDA, 64, float, false>(a, stream);
+  }
+  if (bf16) return kv ? launch_step_t<KDA, 128, __nv_bfloat16, true>(a, stream) : launch_step_t<KDA, 128, __nv_bfloat16, false>(a, stream);
+  return kv ? launch_step_t<KDA, 128, float, true>(a, stream) : launch_step_t<KDA, 128, float, false>(a, stream);
+}
+
+// Checks and fields that both recurrences share.
+static kda_status_t fill_step(StepArgs &a, const void *q, const void *k, const void *v, const void *g, float scale,
+                              void *state, const int32_t *idx, int N, int Hk, int H, int K, int V,
+                              long long num_states, const kda_step_strides_t *st, uint32_t flags, void *o,
+                              bool gate_per_channel) {
+  if (N < 0 || H < 1 || Hk < 1 || K < 1 || V < 1 || num_states < 0 || H % Hk != 0) return KDA_ERR_INVALID_ARG;
+  if (!g || (N > 0 && (!q || !k || !v || !o)) || (num_states > 0 && !state)) return KDA_ERR_INVALID_ARG;
+  if ((K != 64 && K != 128) || (V != 64 && V != 128)) return KDA_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale)) return KDA_ERR_INVALID_ARG;
+  if (!idx && num_states < N) return KDA_ERR_INVALID_ARG;
+  if (!aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(o, 2) || !aligned(state, 16) ||
+      (idx && !aligned(idx, 4)))
+    return KDA_ERR_INVALID_ARG;
+  if ((double)N * H * (V / 32) > 2147483647.0 || (double)num_states * H * K * V > 9.0e15) return KDA_ERR_UNSUPPORTED;
+  std::memset(&a, 0, sizeof a);
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.k = static_cast<const __nv_bfloat16 *>(k);
+  a.v = static_cast<const __nv_bfloat16 *>(v);
+  a.g = g;
+  a.scale = scale;
+  a.state = state;
+  a.idx = idx;
+  a.o = static_cast<__nv_bfloat16 *>(o);
+  a.num_states = num_states;
+  a.N = N;
+  a.H = H;
+  a.group = H / Hk;
+  a.V = V;
+  a.flags = flags;
+  auto set = [&](long long (&dst)[2], const int64_t *src, long long request, long long head) {
+    dst[0] = src ? src[0] : request;
+    dst[1] = src ? src[1] : head;
+  };
+  const long long gw = gate_per_channel ? K : 1;
+  set(a.qs, st ? st->q : nullptr, (long long)Hk * K, K);
+  set(a.ks, st ? st->k : nullptr, (long long)Hk * K, K);
+  set(a.vs, st ? st->v : nullptr, (long long)H * V, V);
+  set(a.gs, st ? st->g : nullptr, (long long)H * gw, gw);
+  set(a.bs, st ? st->beta : nullptr, H, 1);
+  return KDA_OK;
+}
+
+static kda_status_t run_step(bool is_kda, StepArgs &a, int K, kda_stream_t stream) {
+  if (a.N == 0) return KDA_OK;
+  a.dev_status = device_status_address();
+  if (!a.dev_status) return KDA_ERR_CUDA;
+  NvtxRange r(is_kda ? "kda step" : "kda la step");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return (is_kda ? launch_step<true>(a, K, s) : launch_step<false>(a, K, s)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace kda
+
+extern "C" {
+
+kda_status_t kda_step(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                      const float *A_log, const float *dt_bias, float lower_bound, float scale, void *state,
+                      const int32_t *state_indices, int N, int H, int K, int V, int64_t num_states,
+                      const kda_step_strides_t *strides, uint32_t flags, void *o, kda_stream_t stream) {
+  using namespace kda;
+  if (flags & ~(kGatePerHead | kBetaF32 | kStateBf16 | kStateKV)) return KDA_ERR_INVALID_ARG;
+  const bool per_head = flags & kGatePerHead;
+  StepArgs a;
+  const kda_status_t st = fill_step(a, q, k, v, g, scale, state, state_indices, N, H, H, K, V, num_states, strides,
+                                    flags, o, !per_head);
+  if (st != KDA_OK) return st;
+  if (!A_log || (N > 0 && !beta)) return KDA_ERR_INVALID_ARG;
+  if (!std::isfinite(lower_bound) || lower_bound < -5.0f || lower_bound > 0.0f) return KDA_ERR_INVALID_ARG;
+  if (!aligned(g, 2) || !aligned(beta, (flags & kBetaF32) ? 4 : 2) || !aligned(A_log, 4) ||
+      (dt_bias && !aligned(dt_bias, 4)))
+    return KDA_ERR_INVALID_ARG;
+  a.beta = beta;
+  a.A_log = A_log;
+  a.dt_bias = dt_bias;
+  a.lb = lower_bound;
+  return run_step(true, a, K, stream);
+}
+
+kda_status_t kda_la_step(const void *q, const void *k, const void *v, const float *log_decay, float scale,
+                         void *state, const int32_t *state_indices, int N, int Hk, int H, int K, int V,
+                         int64_t num_states, const kda_step_strides_t *strides, uint32_t flags, void *o,
+                         kda_stream_t stream) {
+  using namespace kda;
+  if (flags & ~(kLaTokenDecay | kStateBf16 | kStateKV)) return KDA_ERR_INVALID_ARG;
+  StepArgs a;
+  const kda_status_t st = fill_step(a, q, k, v, log_decay, scale, state, state_indices, N, Hk, H, K, V, num_states,
+                                    strides, flags, o, false);
+  if (st != KDA_OK) return st;
+  if (!aligned(log_decay, 4)) return KDA_ERR_INVALID_ARG;
+  return run_step(false, a, K, stream);
+}
+
+}  // extern "C"

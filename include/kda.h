@@ -81,6 +81,12 @@ typedef enum {
  */
 #define KDA_DEVICE_NONFINITE 3
 
+/*
+ * A state index of kda_step() or kda_la_step() is not below num_states. The
+ * request gets o = 0 and no state is touched.
+ */
+#define KDA_DEVICE_BAD_STATE_INDEX 4
+
 /* Tokens per chunk of the chunked algorithm. */
 #define KDA_CHUNK 64
 
@@ -327,6 +333,149 @@ KDA_API kda_status_t kda_fwd_noalloc(const void *q, const void *k, const void *v
  */
 KDA_API kda_status_t kda_fwd_plan(int B, int T, int H, int K, int V, int num_seqs, int varlen, uint32_t flags,
                                   int *n_segments, int *slice_width);
+
+/* ------------------------------------------------------------------------
+ * Serving operators around the chunked forward. The conventions at the top of
+ * this file hold, with these differences: token tensors may be strided (the
+ * last dimension contiguous), and states may be rows of a pool.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * One token of the KDA recurrence for each of N requests (decoding), on states
+ * kept in a pool. With S the K x V state of pool row state_indices[n]:
+ *
+ *   S <- Diag(alpha) S;  u = beta (v - S^T khat);  S <- S + khat u^T;  o = scale S^T qhat
+ *
+ * with alpha, khat, qhat and beta formed from g, k, q and the logits as in
+ * kda_fwd(): a call per token continues a kda_fwd() whose final_state is the
+ * pool row.
+ *
+ *   q, k, g        bf16 [N,H,K]; v bf16 [N,H,V]; beta bf16 [N,H] logits
+ *                  (KDA_BETA_F32: fp32; KDA_GATE_PER_HEAD: g [N,H], dt_bias [H]).
+ *   A_log, dt_bias, lower_bound, scale  as in kda_fwd().
+ *   state          [num_states,H,V,K] fp32 (KDA_STATE_BF16: bf16;
+ *                  KDA_STATE_KV: [num_states,H,K,V]), updated in place. A bf16
+ *                  state is rounded to nearest-even once per token.
+ *   state_indices  int32 [N], the pool row of each request, or NULL for row n
+ *                  (then num_states >= N). A negative index marks a padding
+ *                  entry: its o is 0 and no state is touched. An index >=
+ *                  num_states does the same and records
+ *                  KDA_DEVICE_BAD_STATE_INDEX. Two entries of one call must
+ *                  not name the same row.
+ *   strides        NULL for contiguous tensors, or element strides of the
+ *                  request and the head dimension (q, k, v, g, beta).
+ *   flags          KDA_GATE_PER_HEAD, KDA_BETA_F32, KDA_STATE_BF16, KDA_STATE_KV.
+ *   o              bf16 [N,H,V], contiguous.
+ *
+ * K and V in {64, 128}. Alignment: state 16 bytes, every other tensor its
+ * element size. No workspace. With N = 0 nothing is launched.
+ */
+typedef struct {
+  int64_t q[2], k[2], v[2], g[2], beta[2];   /* {request, head}, in elements */
+} kda_step_strides_t;
+
+KDA_API kda_status_t kda_step(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                              const float *A_log, const float *dt_bias, float lower_bound, float scale,
+                              void *state, const int32_t *state_indices, int N, int H, int K, int V,
+                              int64_t num_states, const kda_step_strides_t *strides, uint32_t flags, void *o,
+                              kda_stream_t stream);
+
+/*
+ * Linear attention with one decay per head (the fixed-decay linear attention of
+ * the cuLA pages, section "Lightning Attention", and, with a log decay per token,
+ * its gated form), chunked over a prompt. Per sequence and head, tokens in order:
+ *
+ *   S_t = exp(log_decay) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t     (S is K x V)
+ *
+ *   q, k           bf16 [B,T,Hk,K]; value head h reads query / key head
+ *                  h / (H / Hk); H must be a multiple of Hk.
+ *   v              bf16 [B,T,H,V].
+ *   log_decay      fp32 [H], or [B,T,H] with KDA_LA_TOKEN_DECAY; natural
+ *                  logarithms, <= 0. Values below -126 ln 2 (a decay below the
+ *                  smallest normal number, -inf included) count as that.
+ *                  Positive values are taken as they are, and are meaningful
+ *                  while exp of their sum over 128 tokens is finite.
+ *   initial_state, final_state, cu_seqlens, num_seqs   as in kda_fwd_ex()
+ *                  (KDA_STATE_BF16, KDA_STATE_KV); final_state may be
+ *                  initial_state.
+ *   strides        NULL for contiguous tensors, or element strides of batch row,
+ *                  token and head; those of q, k and v (of dimensions longer
+ *                  than 1) positive multiples of 8. log_decay's are used only
+ *                  with KDA_LA_TOKEN_DECAY.
+ *   flags          KDA_LA_TOKEN_DECAY, KDA_STATE_BF16, KDA_STATE_KV.
+ *   o              bf16 [B,T,H,V], contiguous.
+ *   workspace      kda_la_workspace_size() bytes, 256-byte aligned, or NULL to
+ *                  let the call allocate it stream-ordered where it needs any.
+ *
+ * K and V in {64, 128}; T may be 0. Alignment: q, k, v, o and the states 16
+ * bytes, the rest its element size. A malformed cu_seqlens is reported as by
+ * kda_fwd(), and nothing is written. Repeated calls give the same bits.
+ * Token values past a sequence's end, and those of other sequences, never reach
+ * its results, be they infinite or NaN; within a sequence a non-finite k or v
+ * also reaches earlier outputs of its 128-token chunk.
+ */
+#define KDA_LA_TOKEN_DECAY 0x10000u
+
+typedef struct {
+  int64_t q[3], k[3], v[3], log_decay[3];   /* {batch row, token, head}, in elements */
+} kda_la_strides_t;
+
+KDA_API size_t kda_la_workspace_size(int B, int T, int H, int K, int V, int num_seqs, int varlen);
+
+KDA_API kda_status_t kda_la_fwd(const void *q, const void *k, const void *v, const float *log_decay, float scale,
+                                const void *initial_state, void *final_state, const int32_t *cu_seqlens, int B,
+                                int T, int Hk, int H, int K, int V, int num_seqs, const kda_la_strides_t *strides,
+                                uint32_t flags, void *o, void *workspace, size_t workspace_bytes,
+                                kda_stream_t stream);
+
+/*
+ * One token of that linear attention for each of N requests, on states in a
+ * pool: q, k bf16 [N,Hk,K], v bf16 [N,H,V], log_decay fp32 [H] (or [N,H] with
+ * KDA_LA_TOKEN_DECAY). state, state_indices, o and the alignment are those of
+ * kda_step(); strides->g holds the per-token log decay's, beta is not read.
+ * flags: KDA_LA_TOKEN_DECAY, KDA_STATE_BF16, KDA_STATE_KV.
+ */
+KDA_API kda_status_t kda_la_step(const void *q, const void *k, const void *v, const float *log_decay, float scale,
+                                 void *state, const int32_t *state_indices, int N, int Hk, int H, int K, int V,
+                                 int64_t num_states, const kda_step_strides_t *strides, uint32_t flags, void *o,
+                                 kda_stream_t stream);
+
+/*
+ * RMS norm of rows of D values with a gate (the heads' outputs of a layer):
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * weight * act(gate),   act = sigmoid, or SiLU with KDA_NORM_SILU
+ *
+ * x and gate are bf16 [outer,inner,D] with strides {x outer, x inner, gate outer,
+ * gate inner} in elements (NULL: contiguous), weight fp32 [D] or NULL for ones,
+ * y bf16 [outer,inner,D], contiguous; y may be x or gate when that is
+ * contiguous. Statistics and products are fp32, y is rounded once. D from 1 to
+ * 32768, up to 2^31 - 1 rows. Rows with D a multiple of 8 up to 16384, 16-byte
+ * aligned bases and strides that are multiples of 8 run 16 bytes at a time; any
+ * others element by element.
+ */
+#define KDA_NORM_SILU 0x1u
+KDA_API kda_status_t kda_norm_gate(const void *x, const void *gate, const float *weight, float eps, int64_t outer,
+                                   int64_t inner, int D, const int64_t *strides, uint32_t flags, void *y,
+                                   kda_stream_t stream);
+
+/*
+ * The norms around a residual addition, in one pass over rows of D values:
+ *
+ *   z = x;  if post_weight: z = z / sqrt(mean(z^2) + eps) * post_weight;  if gate: z = z sigmoid(gate)
+ *   h = residual + s z,   y = h / sqrt(mean(h^2) + eps) * weight
+ *
+ * with s = scale_vec[D] (fp32) or, where that is NULL, scale. x and gate (or
+ * NULL) are bf16 [rows,D], residual and h bf16 (KDA_NORM_RESIDUAL_F32: fp32),
+ * weight fp32 [D] or NULL for ones, y bf16. strides holds the row strides of x,
+ * residual and gate in elements (NULL: D); y and h are contiguous, and h may be
+ * residual, y may be x or gate, where those are. y is computed from the unrounded
+ * h. Limits, and which rows run 16 bytes at a time, as for kda_norm_gate().
+ */
+#define KDA_NORM_RESIDUAL_F32 0x1u
+KDA_API kda_status_t kda_add_norm(const void *x, const void *residual, const void *gate, const float *post_weight,
+                                  const float *weight, const float *scale_vec, float scale, float eps, int64_t rows,
+                                  int D, const int64_t *strides, uint32_t flags, void *y, void *h,
+                                  kda_stream_t stream);
 
 /* Upper bound on the number of 64-token chunks over all sequences. */
 KDA_API int64_t kda_max_chunks(int B, int T, int num_seqs);
