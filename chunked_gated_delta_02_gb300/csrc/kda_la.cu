@@ -40,6 +40,7 @@
 // Bound: a chunk of one head moves 128 KiB at K = V = 128, 2.9 us of an SM's share of the measured
 // bandwidth, against 48 tensor-core steps of 64 clocks, 1.6 us: memory bandwidth, if loads, products
 // and register work overlap.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -273,8 +274,12 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
   // f(item, head, n): every chunk of this CTA's items, n counting them over all items; begin(item,
   // head, chunks) and end(item, head, chunks) around them. All stop at the first false.
   auto for_chunks = [&](auto &&begin, auto &&chunk, auto &&end) {
+    // The items come longest first: rounds of one item per CTA, every other round backwards, even out
+    // what the CTAs get.
     int n = 0;
-    for (long long w = blockIdx.x; w < total; w += gridDim.x) {
+    for (long long round = 0; round * gridDim.x < total; ++round) {
+      const long long w = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (w >= total) continue;
       const LaItem it = la_item(p, w / p.H);
       const int h = (int)(w % p.H);
       if (AGG && it.seg == it.n_seg - 1) continue;
@@ -746,18 +751,32 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const LaProblem p) {
                                     : static_cast<const float *>(p.init)[i];
     }
   }
-  for (int g = 0; g + 1 < n; ++g) {
-    const long long block = (long long)(slot0 + g) * p.H + h;
-    float4 *at = reinterpret_cast<float4 *>(p.seg_state + block * (K * V)) + x;
-    const float d = p.seg_decay[block];
-    const float4 f = *at;
-    S[0] = fmaf(d, S[0], f.x);
-    S[1] = fmaf(d, S[1], f.y);
-    S[2] = fmaf(d, S[2], f.z);
-    S[3] = fmaf(d, S[3], f.w);
-    *at = make_float4(S[0], S[1], S[2], S[3]);
+  constexpr int kAhead = 8;   // blocks whose loads are in flight together
+  for (int g0 = 0; g0 + 1 < n; g0 += kAhead) {
+    float4 f[kAhead];
+    float d[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (g0 + i + 1 < n) {
+        const long long block = (long long)(slot0 + g0 + i) * p.H + h;
+        f[i] = reinterpret_cast<const float4 *>(p.seg_state + block * (K * V))[x];
+        d[i] = p.seg_decay[block];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (g0 + i + 1 < n) {
+        S[0] = fmaf(d[i], S[0], f[i].x);
+        S[1] = fmaf(d[i], S[1], f[i].y);
+        S[2] = fmaf(d[i], S[2], f[i].z);
+        S[3] = fmaf(d[i], S[3], f[i].w);
+        reinterpret_cast<float4 *>(p.seg_state + ((long long)(slot0 + g0 + i) * p.H + h) * (K * V))[x] =
+            make_float4(S[0], S[1], S[2], S[3]);
+      }
+    }
   }
 }
+
 // Varlen schedule: checks cu_seqlens, cuts the sequences into segments of seg_chunks chunks and lists
 // them longest first (counting sort; very long segments share bins, which only makes the order
 // approximate). One CTA.
@@ -857,13 +876,57 @@ struct LaPlan {
   bool segments;   // whether any sequence may have more than one segment
 };
 
-static LaPlan la_plan(int T, int H, int N, bool varlen) {
+// Time model of a call, in microseconds: `rounds` of items of `chunks` chunks each per CTA, in the
+// kernel that does everything and in the one that forms the segments' states. The constants were
+// measured at K = V = 128 (one item per CTA, many chunks); a chunk takes at least its bytes' share of
+// the memory bandwidth.
+constexpr double kLaChunkUs = 2.6, kLaAggChunkUs = 1.9, kLaItemUs = 2.0, kLaPassUs = 7.0, kLaBytesPerUs = 6.5e6;
+
+static double la_pass_us(long long items, int chunks, int sms, double chunk_us, double chunk_bytes) {
+  if (items == 0) return 0.0;
+  const long long rounds = (items + sms - 1) / sms;
+  const double mem_us = chunk_bytes * (double)std::min(items, (long long)sms) / kLaBytesPerUs;
+  return (double)rounds * (chunks * std::max(chunk_us, mem_us) + kLaItemUs);
+}
+
+// Chunks per segment of `chains` (sequence, head) pairs of nc chunks each: few chains leave SMs idle,
+// and cutting them into segments costs a pass over k and v.
+static int la_segment_chunks(long long chains, int nc, int K, int V, int sms) {
+  const double bytes = kLaChunk * 2.0 * (2 * K + 2 * V), agg_bytes = kLaChunk * 2.0 * (K + V);
+  int best = nc;
+  double best_us = la_pass_us(chains, nc, sms, kLaChunkUs, bytes);
+  for (int n = 2; n <= 512 && n <= nc; ++n) {
+    const int seg = (nc + n - 1) / n, m = (nc + seg - 1) / seg;
+    const double us = la_pass_us(chains * m, seg, sms, kLaChunkUs, bytes) +
+                      la_pass_us(chains * (m - 1), seg, sms, kLaAggChunkUs, agg_bytes) + kLaPassUs;
+    if (us < 0.95 * best_us) {
+      best_us = us;
+      best = seg;
+    }
+  }
+  return best;
+}
+
+static LaPlan la_plan(int T, int H, int K, int V, int N, bool varlen) {
   LaPlan r;
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
   const int nc = std::max(1, (int)(((long long)T + kLaChunk - 1) / kLaChunk));
-  r.seg_chunks = nc;
+  if (!varlen) {
+    r.seg_chunks = la_segment_chunks((long long)N * H, nc, K, V, sms);
+    r.n_seg = (nc + r.seg_chunks - 1) / r.seg_chunks;
+    r.segments = r.n_seg > 1;
+    r.slots = (long long)N * r.n_seg;
+    return r;
+  }
+  // The lengths are on the device: segments as for equal lengths, and never longer than what an SM has
+  // to do on average, so that one long sequence among short ones does not hold up the call.
+  const int nc_mean = std::max(1, (int)(((long long)T / std::max(N, 1) + kLaChunk - 1) / kLaChunk));
+  const int share = (int)std::min((double)nc, std::ceil((nc + 0.5 * N) * (double)H / sms));
+  r.seg_chunks = la_segment_chunks((long long)N * H, nc_mean, K, V, sms);
+  if (r.seg_chunks >= nc_mean) r.seg_chunks = std::max(nc_mean, std::max(share, 8));
   r.n_seg = 1;
-  r.segments = false;
-  r.slots = varlen ? (long long)T / ((long long)r.seg_chunks * kLaChunk) + 2ll * N : (long long)N * r.n_seg;
+  r.segments = r.seg_chunks < nc;
+  r.slots = (long long)T / ((long long)r.seg_chunks * kLaChunk) + 2ll * N;
   return r;
 }
 
@@ -917,9 +980,9 @@ static cudaError_t launch_la(const LaProblem &p, const LaMaps &maps, const LaPla
   if (pl.segments) {
     cudaError_t e = launch_la_t<K, V, true>(p, maps, items, s, overlap);
     if (e == cudaSuccess)
-      e = launch_kernel(la_combine_kernel<K, V>, dim3((unsigned)(p.N * p.H), K * V / 1024), dim3(256), 0, s, false, p);
+      e = launch_kernel(la_combine_kernel<K, V>, dim3((unsigned)(p.N * p.H), K * V / 1024), dim3(256), 0, s, true, p);
     if (e != cudaSuccess) return e;
-    overlap = false;
+    overlap = true;
   }
   return launch_la_t<K, V, false>(p, maps, items, s, overlap);
 }
@@ -935,7 +998,7 @@ extern "C" {
 size_t kda_la_workspace_size(int B, int T, int H, int K, int V, int num_seqs, int varlen) {
   using namespace kda;
   if (!la_sizes_ok(B, T, 1, H, K, V, num_seqs)) return 0;
-  return la_scratch(la_plan(T, H, num_seqs, varlen != 0), H, K, V, num_seqs, varlen != 0).total;
+  return la_scratch(la_plan(T, H, K, V, num_seqs, varlen != 0), H, K, V, num_seqs, varlen != 0).total;
 }
 
 kda_status_t kda_la_fwd(const void *q, const void *k, const void *v, const float *log_decay, float scale,
@@ -968,7 +1031,7 @@ kda_status_t kda_la_fwd(const void *q, const void *k, const void *v, const float
   if ((double)B * T * H * std::max(K, V) > 9.0e15 || (double)num_seqs * H > 2.0e9) return KDA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return KDA_OK;
   const bool varlen = cu_seqlens != nullptr;
-  const LaPlan pl = la_plan(T, H, num_seqs, varlen);
+  const LaPlan pl = la_plan(T, H, K, V, num_seqs, varlen);
   const LaScratch L = la_scratch(pl, H, K, V, num_seqs, varlen);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void *ws = workspace;
