@@ -1,7 +1,9 @@
-"""Build libkda.so (sm_103a) in-tree with nvcc.
+"""Build libkda.so (sm_103a) in-tree with nvcc, and the native binding of the serving operators.
 
 Every .cu file under csrc/ is compiled to an object in parallel, then linked
-into chunked_gated_delta_02_gb300/libkda.so. Only one -gencode target is
+into chunked_gated_delta_02_gb300/libkda.so; binding.cpp is compiled beside them
+with the host compiler against the installed torch, and linked with libkda.so
+into the extension module _serving. Only one -gencode target is
 built: compute_103a / sm_103a (the arch-specific variant is needed for the
 tcgen05 and TMA instructions).
 """
@@ -12,11 +14,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
+BINDING = os.path.join(PKG, "_serving.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr"]
@@ -31,6 +35,26 @@ def nvcc() -> str:
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+
+
+def _torch_dir():
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _binding_compile(obj):
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
+            "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj, "-isystem", inc,
+            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include")]
+
+
+def _binding_link(obj, target):
+    libs = os.path.join(_torch_dir(), "lib")
+    return [os.environ.get("CXX", "g++"), "-shared", "-o", target, obj, "-L" + PKG, "-l:libkda.so", "-L" + libs,
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
 
 
 def _stale(target, deps):
@@ -56,6 +80,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    binding_src = os.path.join(CSRC, "binding.cpp")
+    binding_obj = os.path.join(BUILD, "binding.cpp.o")
+    if force or _stale(binding_obj, [binding_src] + headers):
+        cmd = _binding_compile(binding_obj)
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        procs.append((binding_src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, pr in procs:
         out, _ = pr.communicate()
@@ -66,13 +97,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             sys.stderr.write(text)
     if failed:
         raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
-    if force or _stale(LIB, objs):
-        tmp = LIB + f".tmp{os.getpid()}"
-        cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"]
-        r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-        if r.returncode != 0:
-            raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
-        os.replace(tmp, LIB)
+    for target, deps, command in (
+            (LIB, objs, lambda tmp: [nvcc()] + ARCH + ["-shared", "-Xlinker", "-soname=libkda.so", "-o", tmp] + objs + ["-lcudart"]),
+            (BINDING, [binding_obj, LIB], lambda tmp: _binding_link(binding_obj, tmp))):
+        if force or _stale(target, deps):
+            tmp = target + f".tmp{os.getpid()}"
+            r = subprocess.run(command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+            if r.returncode != 0:
+                raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
+            os.replace(tmp, target)
     return LIB
 
 
