@@ -1008,7 +1008,7 @@ kda_status_t kda_la_fwd(const void *q, const void *k, const void *v, const float
   using namespace kda;
   if (flags & ~(kLaTokenDecay | kStateBf16 | kStateKV)) return KDA_ERR_INVALID_ARG;
   if (!la_sizes_ok(B, T, Hk, H, K, V, num_seqs)) return KDA_ERR_INVALID_ARG;
-  if (!log_decay || (T > 0 && (!q || !k || !v || !o))) return KDA_ERR_INVALID_ARG;
+  if (T > 0 && (!q || !k || !v || !log_decay || !o)) return KDA_ERR_INVALID_ARG;
   if ((K != 64 && K != 128) || (V != 64 && V != 128)) return KDA_ERR_UNSUPPORTED;
   if (!std::isfinite(scale)) return KDA_ERR_INVALID_ARG;
   if (cu_seqlens ? (B != 1 || !aligned(cu_seqlens, 4)) : num_seqs != B) return KDA_ERR_INVALID_ARG;
@@ -1025,7 +1025,7 @@ kda_status_t kda_la_fwd(const void *q, const void *k, const void *v, const float
     const int64_t *s3[3] = {sq, sk, sv};
     for (int x = 0; x < 3; ++x) {
       const int64_t n = i < 2 ? extent[i] : (x == 2 ? H : Hk);
-      if (n > 1 && (s3[x][i] < 0 || s3[x][i] % 8 != 0 || s3[x][i] >= (int64_t)1 << 39)) return KDA_ERR_INVALID_ARG;
+      if (n > 1 && (s3[x][i] <= 0 || s3[x][i] % 8 != 0 || s3[x][i] >= (int64_t)1 << 39)) return KDA_ERR_INVALID_ARG;
     }
   }
   if ((double)B * T * H * std::max(K, V) > 9.0e15 || (double)num_seqs * H > 2.0e9) return KDA_ERR_UNSUPPORTED;

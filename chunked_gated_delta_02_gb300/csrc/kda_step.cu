@@ -333,7 +333,7 @@ static kda_status_t fill_step(StepArgs &a, const void *q, const void *k, const v
                               long long num_states, const kda_step_strides_t *st, uint32_t flags, void *o,
                               bool gate_per_channel) {
   if (N < 0 || H < 1 || Hk < 1 || K < 1 || V < 1 || num_states < 0 || H % Hk != 0) return KDA_ERR_INVALID_ARG;
-  if (!g || (N > 0 && (!q || !k || !v || !o)) || (num_states > 0 && !state)) return KDA_ERR_INVALID_ARG;
+  if ((N > 0 && (!q || !k || !v || !g || !o)) || (num_states > 0 && !state)) return KDA_ERR_INVALID_ARG;
   if ((K != 64 && K != 128) || (V != 64 && V != 128)) return KDA_ERR_UNSUPPORTED;
   if (!std::isfinite(scale)) return KDA_ERR_INVALID_ARG;
   if (!idx && num_states < N) return KDA_ERR_INVALID_ARG;
