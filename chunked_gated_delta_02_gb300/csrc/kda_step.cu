@@ -43,34 +43,31 @@ struct StepArgs {
   uint32_t flags;
 };
 
-// 16 bytes of state: 4 fp32 or 8 bf16 values.
+// 16 bytes of state, 4 fp32 or 8 bf16 values, as pairs for the packed fp32 instructions.
 template <typename ST> struct StateVec;
 template <> struct StateVec<float> {
   static constexpr int n = 4;
-  __device__ static __forceinline__ void unpack(const uint4 &r, float (&x)[4]) {
-    x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y);
-    x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
+  __device__ static __forceinline__ void unpack(const uint4 &r, float2 (&x)[2]) {
+    x[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+    x[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
   }
-  __device__ static __forceinline__ uint4 pack(const float (&x)[4]) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  __device__ static __forceinline__ uint4 pack(const float2 (&x)[2]) {
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x), __float_as_uint(x[1].y));
   }
 };
 template <> struct StateVec<__nv_bfloat16> {
   static constexpr int n = 8;
-  __device__ static __forceinline__ void unpack(const uint4 &r, float (&x)[8]) {
+  __device__ static __forceinline__ void unpack(const uint4 &r, float2 (&x)[4]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
   }
   // the one rounding of a bf16 state per token, to nearest even
-  __device__ static __forceinline__ uint4 pack(const float (&x)[8]) {
+  __device__ static __forceinline__ uint4 pack(const float2 (&x)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[i].x, x[i].y);
       w[i] = *reinterpret_cast<const uint32_t *>(&b);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -78,13 +75,15 @@ template <> struct StateVec<__nv_bfloat16> {
 };
 
 template <int N>
-__device__ __forceinline__ void load_shared(const float *src, float (&x)[N]) {
+__device__ __forceinline__ void load_shared(const float *src, float2 (&x)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const float4 f = *reinterpret_cast<const float4 *>(src + i);
-    x[i] = f.x; x[i + 1] = f.y; x[i + 2] = f.z; x[i + 3] = f.w;
+  for (int i = 0; i < N; i += 2) {
+    const float4 f = *reinterpret_cast<const float4 *>(src + 2 * i);
+    x[i] = make_float2(f.x, f.y);
+    x[i + 1] = make_float2(f.z, f.w);
   }
 }
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
 
 // Tile of one CTA: R rows x CB columns of the stored matrix, CB along the contiguous dimension.
 //   [V, K] layout: rows are value columns v, a row holds all K channels (CB = K);
@@ -101,14 +100,21 @@ struct StepTile {
   static constexpr int slice = KV ? cols : rows;                         // value columns per CTA
 };
 
+// CTAs per SM the registers are fitted to. Six keep 96 KiB of loads in flight. KDA on a bf16 state has
+// twice the values per byte and their three factors to hold: fitted to six it spills and takes 110.7 us
+// for 200 requests of 32 heads at K = V = 128, fitted to four 74.4 us (floor 63.1 us; fp32 state, six:
+// 124.4 us, floor 125.0 us).
+template <bool KDA, typename ST>
+constexpr int kStepCtas = (KDA && sizeof(ST) == 2) ? 4 : 6;
+
 template <bool KDA, int K, typename ST, bool KV>
-__global__ void __launch_bounds__(kStepThreads, 6) step_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(kStepThreads, kStepCtas<KDA, ST>) step_kernel(const StepArgs a) {
   using T = StepTile<K, ST, KV>;
   using Vec = StateVec<ST>;
   constexpr int kVec = T::vec;
   __shared__ __align__(16) float s_q[K], s_k[K], s_a[K], s_v[T::slice];
   __shared__ float s_part[3][kStepWarps];
-  __shared__ float s_red[KV ? 2 : 1][KV ? kStepWarps : 1][T::slice];   // [K, V] layout: sums over the warps
+  __shared__ __align__(16) float s_red[KV ? 2 : 1][KV ? kStepWarps : 1][T::slice];   // [K, V] layout: sums over the warps
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slices = a.V / T::slice;
@@ -180,120 +186,122 @@ __global__ void __launch_bounds__(kStepThreads, 6) step_kernel(const StepArgs a)
     qk = sums[2] * rq * rk;
   }
 
+  constexpr int kPairs = kVec / 2;
   if constexpr (!KV) {
-    // Rows are value columns: the products over k are sums over a lane's values and 8 lanes.
+    // Rows are value columns: the products over k are sums over a lane's values and 8 lanes. A
+    // lane's channels are the same in every row, so their factors stay in registers: read per row,
+    // they would take more shared-memory time than the state takes from memory.
+    float2 kk[T::per_row][kPairs], qq[T::per_row][kPairs], aa[KDA ? T::per_row : 1][kPairs];
+#pragma unroll
+    for (int j = 0; j < T::per_row; ++j) {
+      load_shared(s_k + j * T::span + c * kVec, kk[j]);
+      load_shared(s_q + j * T::span + c * kVec, qq[j]);
+      if constexpr (KDA) load_shared(s_a + j * T::span + c * kVec, aa[j]);
+    }
 #pragma unroll
     for (int p = 0; p < T::passes; ++p) {
       const int vi = p * 16 + r;
       const float vv = s_v[vi];
-      float x[T::per_row][kVec];
-      float d1 = 0.f, d2 = 0.f;
+      float2 x[T::per_row][kPairs];
+      float2 d1 = splat(0.f), d2 = splat(0.f);
 #pragma unroll
       for (int j = 0; j < T::per_row; ++j) {
-        const int k0 = j * T::span + c * kVec;
-        float kk[kVec], qq[kVec];
-        load_shared(s_k + k0, kk);
-        load_shared(s_q + k0, qq);
         Vec::unpack(raw[p][j], x[j]);
-        if constexpr (KDA) {
-          float aa[kVec];
-          load_shared(s_a + k0, aa);
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            x[j][e] *= aa[e];
-            d1 = fmaf(kk[e], x[j][e], d1);
-            d2 = fmaf(qq[e], x[j][e], d2);
+        for (int e = 0; e < kPairs; ++e) {
+          if constexpr (KDA) {
+            x[j][e] = __fmul2_rn(aa[j][e], x[j][e]);
+            d1 = __ffma2_rn(kk[j][e], x[j][e], d1);
+          } else {
+            x[j][e] = __ffma2_rn(splat(decay), x[j][e], __fmul2_rn(kk[j][e], splat(vv)));
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            x[j][e] = fmaf(decay, x[j][e], kk[e] * vv);
-            d2 = fmaf(qq[e], x[j][e], d2);
-          }
+          d2 = __ffma2_rn(qq[j][e], x[j][e], d2);
         }
       }
+      float s1 = d1.x + d1.y, s2 = d2.x + d2.y;
 #pragma unroll
       for (int m = 1; m < 8; m <<= 1) {
-        if constexpr (KDA) d1 += __shfl_xor_sync(0xffffffffu, d1, m);
-        d2 += __shfl_xor_sync(0xffffffffu, d2, m);
+        if constexpr (KDA) s1 += __shfl_xor_sync(0xffffffffu, s1, m);
+        s2 += __shfl_xor_sync(0xffffffffu, s2, m);
       }
-      float out = d2;
       if constexpr (KDA) {
-        const float u = beta * (vv - rk * d1);
-        const float ku = rk * u;
-        out = fmaf(qk, u, rq * d2);
+        const float u = beta * (vv - rk * s1);
+        s2 = fmaf(qk, u, rq * s2);
+        const float2 ku = splat(rk * u);
 #pragma unroll
-        for (int j = 0; j < T::per_row; ++j) {
-          float kk[kVec];
-          load_shared(s_k + j * T::span + c * kVec, kk);
+        for (int j = 0; j < T::per_row; ++j)
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) x[j][e] = fmaf(ku, kk[e], x[j][e]);
-        }
+          for (int e = 0; e < kPairs; ++e) x[j][e] = __ffma2_rn(ku, kk[j][e], x[j][e]);
       }
 #pragma unroll
       for (int j = 0; j < T::per_row; ++j)
         __stcs(reinterpret_cast<uint4 *>(tile + vi * ld + j * T::span + c * kVec), Vec::pack(x[j]));
-      if (c == 0) o[vi] = __float2bfloat16_rn(a.scale * out);
+      if (c == 0) o[vi] = __float2bfloat16_rn(a.scale * s2);
     }
   } else {
     // Rows are channels k: the products over k are sums over a lane's rows, 4 lanes and the warps.
-    float d1[kVec], d2[kVec], vv[kVec];
+    float2 d1[kPairs], d2[kPairs], vv[kPairs];
     load_shared(s_v + c * kVec, vv);
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) d1[e] = d2[e] = 0.f;
+    for (int e = 0; e < kPairs; ++e) d1[e] = d2[e] = splat(0.f);
 #pragma unroll
     for (int p = 0; p < T::passes; ++p) {
       const int k = p * 16 + r;
-      const float kk = s_k[k], qq = s_q[k];
-      float x[kVec];
+      const float2 kk = splat(s_k[k]), qq = splat(s_q[k]);
+      float2 x[kPairs];
       Vec::unpack(raw[p][0], x);
       if constexpr (KDA) {
-        const float aa = s_a[k];
+        const float2 aa = splat(s_a[k]);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const float s = aa * x[e];
-          d1[e] = fmaf(kk, s, d1[e]);
-          d2[e] = fmaf(qq, s, d2[e]);
+        for (int e = 0; e < kPairs; ++e) {
+          const float2 t = __fmul2_rn(aa, x[e]);
+          d1[e] = __ffma2_rn(kk, t, d1[e]);
+          d2[e] = __ffma2_rn(qq, t, d2[e]);
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          x[e] = fmaf(decay, x[e], kk * vv[e]);
-          d2[e] = fmaf(qq, x[e], d2[e]);
+        for (int e = 0; e < kPairs; ++e) {
+          x[e] = __ffma2_rn(splat(decay), x[e], __fmul2_rn(kk, vv[e]));
+          d2[e] = __ffma2_rn(qq, x[e], d2[e]);
         }
         __stcs(reinterpret_cast<uint4 *>(tile + k * ld + c * kVec), Vec::pack(x));
       }
     }
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
+    for (int e = 0; e < kPairs; ++e) {
 #pragma unroll
       for (int m = 8; m < 32; m <<= 1) {
-        if constexpr (KDA) d1[e] += __shfl_xor_sync(0xffffffffu, d1[e], m);
-        d2[e] += __shfl_xor_sync(0xffffffffu, d2[e], m);
+        if constexpr (KDA) {
+          d1[e].x += __shfl_xor_sync(0xffffffffu, d1[e].x, m);
+          d1[e].y += __shfl_xor_sync(0xffffffffu, d1[e].y, m);
+        }
+        d2[e].x += __shfl_xor_sync(0xffffffffu, d2[e].x, m);
+        d2[e].y += __shfl_xor_sync(0xffffffffu, d2[e].y, m);
       }
       if (lane < 8) {
-        s_red[0][warp][c * kVec + e] = d2[e];
-        if constexpr (KDA) s_red[1][warp][c * kVec + e] = d1[e];
+        *reinterpret_cast<float2 *>(&s_red[0][warp][c * kVec + 2 * e]) = d2[e];
+        if constexpr (KDA) *reinterpret_cast<float2 *>(&s_red[1][warp][c * kVec + 2 * e]) = d1[e];
       }
     }
     __syncthreads();
     if constexpr (KDA) {
-      float u[kVec];
+      float2 u[kPairs];   // rk u of this lane's columns
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        float s = 0.f;
+      for (int e = 0; e < kPairs; ++e) {
+        float2 t = splat(0.f);
 #pragma unroll
-        for (int w = 0; w < kStepWarps; ++w) s += s_red[1][w][c * kVec + e];
-        u[e] = beta * (vv[e] - rk * s);
+        for (int w = 0; w < kStepWarps; ++w)
+          t = __fadd2_rn(t, *reinterpret_cast<const float2 *>(&s_red[1][w][c * kVec + 2 * e]));
+        u[e] = __fmul2_rn(splat(beta * rk), __ffma2_rn(splat(-rk), t, vv[e]));
       }
 #pragma unroll
       for (int p = 0; p < T::passes; ++p) {
         const int k = p * 16 + r;
-        const float ku = rk * s_k[k], aa = s_a[k];
-        float x[kVec];
+        const float2 kk = splat(s_k[k]), aa = splat(s_a[k]);
+        float2 x[kPairs];
         Vec::unpack(raw[p][0], x);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) x[e] = fmaf(ku, u[e], aa * x[e]);
+        for (int e = 0; e < kPairs; ++e) x[e] = __ffma2_rn(kk, u[e], __fmul2_rn(aa, x[e]));
         __stcs(reinterpret_cast<uint4 *>(tile + k * ld + c * kVec), Vec::pack(x));
       }
     }
