@@ -66,17 +66,20 @@ constexpr float kLaRowLog2 = -64.0f;
 
 // Decay factors of one chunk.
 struct LaGate {
-  float G[kLaChunk];    // log2 decay from the chunk's start through token i
+  // G_i, the log2 decay from the chunk's start through token i; in a weak chunk, whose decay stays
+  // above 2^-64, the factor 2^-G_i itself
+  float G[kLaChunk];
   float cf[kLaChunk];   // decay from token j to the end of its 32-token block; 0 past the sequence
   float bf[4];          // decay from the end of 32-token block c to the chunk's end
   float gamma;          // decay of the whole chunk
-  float pad[3];
+  int weak;
+  float pad[2];
 };
 
 struct LaMisc {
   // per stage: q, k and the decay factors ready and consumed; the same of v, whose buffer then holds
-  // the output tile; v rows past the sequence cleared; output tile written
-  uint64_t full[3], empty[3], full_v[3], empty_v[3], v_rdy[3], o_st[3];
+  // the output tile; v rows past the sequence cleared; V' formed; output tile written
+  uint64_t full[3], empty[3], full_v[3], empty_v[3], v_rdy[3], v_read[3], o_st[3];
   uint64_t p_raw, p_rdy, s_free, o_done, o_free, d_rdy, d_free, s_rdy;   // one phase per chunk
   uint64_t vp_rdy[2], vp_free[2];                   // per V' buffer: 32 tokens ready, read
   uint64_t bar_exit;
@@ -217,6 +220,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       umma::mbar_init(&ms.v_rdy[s], 4);
+      umma::mbar_init(&ms.v_read[s], 4);
       umma::mbar_init(&ms.full[s], 2);        // the loads' issuer and the factors' writer
       umma::mbar_init(&ms.empty[s], (AGG ? 1 : 2) + 8);   // M4, M3 and the eight state warps
       umma::mbar_init(&ms.full_v[s], 1);
@@ -350,10 +354,11 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
       const float later = __shfl_down_sync(0xffffffffu, after, 1);
       const float tail = (lane & 7) == 7 ? 0.f : later;
       LaGate &g = gates[st];
+      const bool weak = __shfl_sync(0xffffffffu, incl, 31) >= kLaRowLog2;   // so are all sums, for decays <= 1
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = 4 * lane + e;
-        g.G[i] = before + pre[e];
+        g.G[i] = weak ? ex2_approx(-(before + pre[e])) : before + pre[e];
         g.cf[i] = i < L ? ex2_approx(suf[e] + tail) : 0.f;
       }
       const float b1 = __shfl_sync(0xffffffffu, block, 8), b2 = __shfl_sync(0xffffffffu, block, 16),
@@ -364,6 +369,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
         g.bf[2] = ex2_approx(b3);
         g.bf[3] = 1.f;
         g.gamma = ex2_approx(b0 + b1 + b2 + b3);
+        g.weak = weak;
       }
       __syncwarp();
       if (lane == 0) umma::mbar_arrive(&ms.full[st]);
@@ -494,42 +500,41 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
         const int st = (int)(n % kStages);
         if (!wait(&ms.full[st], (uint32_t)((n / kStages) & 1))) return false;
         const LaGate &g = gates[st];
-        const bool weak = g.G[kLaChunk - 1] >= kLaRowLog2;   // so are all sums of the chunk, for decays <= 1
-        const float Gi = g.G[row], Gr = Gi - fmaxf(Gi, kLaRowLog2);   // G_i - R_i
+        const bool weak = g.weak != 0;
+        const float Gr = weak ? 0.f : g.G[row] - fmaxf(g.G[row], kLaRowLog2);   // G_i - R_i
         if (!wait(&ms.p_raw, (uint32_t)(n & 1))) return false;
+        // Rolled over 32-column blocks: a warp runs its role alone on its scheduler, and code that does not
+        // repeat is fetched at every step (unrolled, with loads a block ahead, P took twice as long).
+#pragma unroll 1
+        for (int c = 0; c <= warp; ++c) {
+          float x[32];
+          umma::tmem_ld32(tmem + kTmP + lane_base + c * 32, x);
+          umma::tmem_ld_wait();
+          if (weak) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-          if (c <= warp) {
-            float x[32];
-            umma::tmem_ld32(tmem + kTmP + lane_base + c * 32, x);
-            umma::tmem_ld_wait();
-            if (weak || c < warp) {
-              // exp(G_i - R_i - G_j) as the decay from j to its block's end and one factor of the block
-              const float f = ex2_approx(Gr - g.G[32 * c + 31]);
-              const float2 f2 = make_float2(f, f);
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 cf = *reinterpret_cast<const float4 *>(&g.cf[32 * c + j]);
-                const float2 a = __fmul2_rn(make_float2(x[j], x[j + 1]), __fmul2_rn(make_float2(cf.x, cf.y), f2));
-                const float2 b = __fmul2_rn(make_float2(x[j + 2], x[j + 3]), __fmul2_rn(make_float2(cf.z, cf.w), f2));
-                x[j] = a.x; x[j + 1] = a.y; x[j + 2] = b.x; x[j + 3] = b.y;
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] *= ex2_approx(Gr - g.G[32 * c + j]);
+            for (int j = 0; j < 32; j += 4) {
+              const float4 w = *reinterpret_cast<const float4 *>(&g.G[32 * c + j]);
+              const float2 a = __fmul2_rn(make_float2(x[j], x[j + 1]), make_float2(w.x, w.y));
+              const float2 b = __fmul2_rn(make_float2(x[j + 2], x[j + 3]), make_float2(w.z, w.w));
+              x[j] = a.x; x[j + 1] = a.y; x[j + 2] = b.x; x[j + 3] = b.y;
             }
-            if (c == warp) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) pk[j] = 0u;
+            for (int j = 0; j < 32; ++j) x[j] *= ex2_approx(Gr - g.G[32 * c + j]);
           }
+          if (c == warp) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
+          }
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
           umma::tmem_st16(tmem + kTmP + lane_base + c * 16, pk);
+        }
+#pragma unroll 1
+        for (int c = 2 * warp + 2; c < 8; ++c) {
+          const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+          umma::tmem_st8(tmem + kTmP + lane_base + c * 8, zero);
         }
         umma::tmem_st_wait();
         arrive(&ms.p_rdy);
@@ -564,38 +569,50 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
       // this warp's 16 channels x 16 tokens; lane l names token l % 8 of matrix l / 8
       const int ch0 = (warp & 3) * 32 + ((lane >> 3) & 1) * 8;
       const uint32_t src = umma::smem_u32(vt) + (ch0 >> 6) * Lay::panel + ((lane >> 4) * 8 + (lane & 7)) * 128;
+      uint32_t raw[16];   // of 32 tokens: [16 channels][8-token block][8 channels]
+      auto load = [&](int b) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            umma::ldmatrix_x4_trans(src + (32 * b + 16 * i) * 128 + (uint32_t)(((((ch0 & 63) >> 3) + 2 * hh) ^ (lane & 7)) << 4),
+                                    raw[8 * hh + 4 * i], raw[8 * hh + 4 * i + 1], raw[8 * hh + 4 * i + 2], raw[8 * hh + 4 * i + 3]);
+      };
+      const bool has_ch = (warp & 3) * 32 < V;
+      if (has_ch) load(0);
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
         const int buf = b & 1;
-        // M4 has read the buffer's last content (two phases per chunk: the one before this is b / 2 - 1)
-        if ((n > 0 || b >= 2) && !wait(&ms.vp_free[buf], (uint32_t)((b >> 1) ^ 1))) return false;
-        if ((warp & 3) * 32 < V) {
+        uint32_t t0[16], t1[16], t2[16];
+        if (has_ch) {
           const float bf = g.bf[b];
-          float2 w[4];   // factors of tokens 8 m + 2 (l % 4) and the next
+          const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
-            w[m] = __fmul2_rn(*reinterpret_cast<const float2 *>(&g.cf[32 * b + 8 * m + 2 * (lane & 3)]), make_float2(bf, bf));
+          for (int m = 0; m < 4; ++m) {   // factors of tokens 8 m + 2 (l % 4) and the next
+            const float2 w = __fmul2_rn(*reinterpret_cast<const float2 *>(&g.cf[32 * b + 8 * m + 2 * (lane & 3)]), make_float2(bf, bf));
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {   // 16 channels each
-            uint32_t raw[8], t0[8], t1[8], t2[8];
-            const uint32_t c16 = (uint32_t)(((((ch0 & 63) >> 3) + 2 * hh) ^ (lane & 7)) << 4);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              umma::ldmatrix_x4_trans(src + (32 * b + 16 * i) * 128 + c16, raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
-            const float2 minus = make_float2(-1.f, -1.f);
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {   // token pairs 8 (r / 2) of channels 8 (r % 2)
-              float2 x = __fmul2_rn(make_float2(__uint_as_float(raw[r] << 16), __uint_as_float(raw[r] & 0xFFFF0000u)), w[r >> 1]);
+            for (int e = 0; e < 4; ++e) {   // token pairs of channels 16 (e / 2) + 8 (e % 2)
+              const int r = 8 * (e >> 1) + 2 * m + (e & 1);
+              float2 x = __fmul2_rn(make_float2(__uint_as_float(raw[r] << 16), __uint_as_float(raw[r] & 0xFFFF0000u)), w);
               t0[r] = pack_bf16(x.x, x.y);
               x = __ffma2_rn(make_float2(__uint_as_float(t0[r] << 16), __uint_as_float(t0[r] & 0xFFFF0000u)), minus, x);
               t1[r] = pack_bf16(x.x, x.y);
               x = __ffma2_rn(make_float2(__uint_as_float(t1[r] << 16), __uint_as_float(t1[r] & 0xFFFF0000u)), minus, x);
               t2[r] = pack_bf16(x.x, x.y);
             }
+          }
+          if (b < 3) load(b + 1);
+        }
+        if (b == 3 && !AGG) arrive(&ms.v_read[st]);
+        // M4 has read the buffer's last content (two phases per chunk: the one before this is b / 2 - 1)
+        if ((n > 0 || b >= 2) && !wait(&ms.vp_free[buf], (uint32_t)((b >> 1) ^ 1))) return false;
+        if (has_ch) {
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {   // 16 channels each
             const uint32_t dst = tmem + kTmVp + buf * kTmVpBuf + lane_base + ((uint32_t)(hh * 16) << 16);
-            umma::tmem_st_16x128b_x4(dst, t0);
-            umma::tmem_st_16x128b_x4(dst + 16, t1);
-            umma::tmem_st_16x128b_x4(dst + 32, t2);
+            umma::tmem_st_16x128b_x4(dst, t0 + 8 * hh);
+            umma::tmem_st_16x128b_x4(dst + 16, t1 + 8 * hh);
+            umma::tmem_st_16x128b_x4(dst + 32, t2 + 8 * hh);
           }
           umma::tmem_st_wait();
         }
@@ -611,19 +628,13 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
     const bool has_v = (warp & 3) * 32 < V;    // lanes are value columns of S^T, token rows of O
     float S[KH];
     float seg_decay = 1.f;
-    auto write_s = [&] {                       // bf16 copy of S^T, the operand of M2
-      if constexpr (!AGG) {
-        if (has_v) {
+    auto copy_s = [&](int x) {                 // bf16 copy of columns x .. x + 31 of S^T, the operand of M2
 #pragma unroll
-          for (int x = 0; x < KH / 8; ++x) {
-            const int k = half * KH + x * 8;
-            *reinterpret_cast<uint4 *>(sm + Lay::s_off + (k >> 6) * Lay::s_panel + umma::sw128_chunk(row, (k & 63) >> 3)) =
-                make_uint4(pack_bf16(S[8 * x], S[8 * x + 1]), pack_bf16(S[8 * x + 2], S[8 * x + 3]),
-                           pack_bf16(S[8 * x + 4], S[8 * x + 5]), pack_bf16(S[8 * x + 6], S[8 * x + 7]));
-          }
-        }
-        umma::fence_proxy_async_smem();
-        arrive(&ms.s_rdy);
+      for (int j = x; j < x + 32; j += 8) {
+        const int k = half * KH + j;
+        *reinterpret_cast<uint4 *>(sm + Lay::s_off + (k >> 6) * Lay::s_panel + umma::sw128_chunk(row, (k & 63) >> 3)) =
+            make_uint4(pack_bf16(S[j], S[j + 1]), pack_bf16(S[j + 2], S[j + 3]), pack_bf16(S[j + 4], S[j + 5]),
+                       pack_bf16(S[j + 6], S[j + 7]));
       }
     };
     auto seg_block = [&](int slot, int h) { return p.seg_state + ((long long)slot * p.H + h) * (K * V); };
@@ -643,7 +654,14 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
             }
           }
           seg_decay = 1.f;
-          if (nch > 0) write_s();   // M2 of the item before has read its copy (s_free)
+          if (!AGG && nch > 0) {   // M2 of the item before has read its copy (s_free)
+            if (has_v) {
+#pragma unroll
+              for (int x = 0; x < KH; x += 32) copy_s(x);
+            }
+            umma::fence_proxy_async_smem();
+            arrive(&ms.s_rdy);
+          }
           return true;
         },
         [&](const LaItem &it, int h, int c, int nch, int n) {
@@ -652,55 +670,70 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           if (!wait(&ms.full[st], (uint32_t)((n / kStages) & 1))) return false;
           const float gamma = gates[st].gamma;
           float f = 0.f;   // scale exp(R_i) of this thread's token row
-          if constexpr (!AGG) f = p.scale * ex2_approx(fmaxf(gates[st].G[row], kLaRowLog2));
+          if constexpr (!AGG) {
+            const float G = gates[st].G[row];
+            f = p.scale * (gates[st].weak ? rcp_approx(G) : ex2_approx(fmaxf(G, kLaRowLog2)));
+          }
           arrive(&ms.empty[st]);   // the factors have been read
-          if (!wait(&ms.d_rdy, ph)) return false;
-          if (has_v) {
+          auto new_state = [&] {   // S^T = gamma S^T + D^T, and its copy for the next chunk
+            if (!wait(&ms.d_rdy, ph)) return false;
+            const bool copy = !AGG && c + 1 < nch;
+            if (!AGG && !wait(&ms.s_free, ph)) return false;   // M2 has read the copy of S
+            if (has_v) {
 #pragma unroll
-            for (int x = 0; x < KH; x += 16) {
-              float y[16];
-              umma::tmem_ld16(tmem + kTmD + lane_base + half * KH + x, y);
-              umma::tmem_ld_wait();
+              for (int x = 0; x < KH; x += 32) {
+                float y[32];
+                umma::tmem_ld32(tmem + kTmD + lane_base + half * KH + x, y);
+                umma::tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                const float2 a = __ffma2_rn(make_float2(gamma, gamma), make_float2(S[x + j], S[x + j + 1]), make_float2(y[j], y[j + 1]));
-                S[x + j] = a.x;
-                S[x + j + 1] = a.y;
+                for (int j = 0; j < 32; j += 2) {
+                  const float2 a = __ffma2_rn(make_float2(gamma, gamma), make_float2(S[x + j], S[x + j + 1]), make_float2(y[j], y[j + 1]));
+                  S[x + j] = a.x;
+                  S[x + j + 1] = a.y;
+                }
+                if (copy) copy_s(x);
               }
             }
-          }
-          arrive(&ms.d_free);
-          if constexpr (AGG) seg_decay *= gamma;
-          if constexpr (!AGG) {
-            if (!wait(&ms.s_free, ph)) return false;   // M2 has read the copy of S
-          }
-          if (c + 1 < nch) write_s();
-          if constexpr (!AGG) {
-            if (!wait(&ms.o_done, ph)) return false;
-            // o in bf16 over the chunk's v: M3 has read it, and so have the V' warps (d_rdy)
+            arrive(&ms.d_free);
+            if constexpr (AGG) seg_decay *= gamma;
+            if (copy) {
+              umma::fence_proxy_async_smem();
+              arrive(&ms.s_rdy);
+            }
+            return true;
+          };
+          auto output = [&] {      // o in bf16 over the chunk's v, which M3 and the V' warps have read
+            if (!wait(&ms.o_done, ph) || !wait(&ms.v_read[st], (uint32_t)((n / kStages) & 1))) return false;
             unsigned char *tile = sm + st * Lay::stage + Lay::v_off;
 #pragma unroll 1
             for (int x = 0; x < VH; x += 32) {
               float y[32];
               umma::tmem_ld32(tmem + kTmO + lane_base + half * VH + x, y);
               umma::tmem_ld_wait();
-              if (x + 32 >= VH) arrive(&ms.o_free);
-#pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                const float2 a = __fmul2_rn(make_float2(y[j], y[j + 1]), make_float2(f, f));
-                y[j] = a.x;
-                y[j + 1] = a.y;
-              }
               const int col = half * VH + x;
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
+              for (int j = 0; j < 4; ++j) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 a = __fmul2_rn(make_float2(y[8 * j + 2 * e], y[8 * j + 2 * e + 1]), make_float2(f, f));
+                  pk[e] = pack_bf16(a.x, a.y);
+                }
                 *reinterpret_cast<uint4 *>(tile + (col >> 6) * Lay::panel + umma::sw128_chunk(row, ((col & 63) >> 3) + j)) =
-                    make_uint4(pack_bf16(y[8 * j], y[8 * j + 1]), pack_bf16(y[8 * j + 2], y[8 * j + 3]),
-                               pack_bf16(y[8 * j + 4], y[8 * j + 5]), pack_bf16(y[8 * j + 6], y[8 * j + 7]));
+                    make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              }
             }
+            arrive(&ms.o_free);
             umma::fence_proxy_async_smem();
             arrive(&ms.o_st[st]);
-          }
+            return true;
+          };
+          if constexpr (AGG) return new_state();
+          // whichever product is done first; rolled, so that each part is one piece of code
+          const bool state_first = __all_sync(0xffffffffu, umma::mbar_test(&ms.d_rdy, ph));
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part)
+            if (!((part == 0) == state_first ? new_state() : output())) return false;
           return true;
         },
         [&](const LaItem &it, int h, int) {
