@@ -27,9 +27,9 @@
 // A CTA takes (sequence segment, head) items, all V columns at once, so that q, k and v are read
 // once; it is persistent over items (one CTA per SM: two stages of q, k and v and S fill the
 // shared memory). Warp roles, coupled by mbarriers only:
-//   warps 0-3    P, in place of the scores in tensor memory (A operand of M3)
-//   warps 4-7    V': transposed from the v tile into tensor memory (A operand of M4), 32 tokens at
-//                a time into two buffers in turn
+//   warps 0-7    P, in place of the scores in tensor memory (A operand of M3), each warpgroup every
+//                other 32 columns; V', transposed from the v tile into tensor memory (A operand of
+//                M4), each warpgroup every other 32 tokens, with a buffer of its own
 //   warps 8-15   the state, and the scaled output in bf16
 //   warp 16      loads (TMA, 128-byte swizzle) and the chunk's decay factors
 //   warp 17      issues M1, M2 and M3;  warp 18  issues M4
@@ -54,8 +54,8 @@ namespace kda {
 constexpr int kLaThreads = 640;
 // Registers per thread by warpgroup; a block is launched with 96 for each of its threads, and the
 // state warps' increase is what the others give back: 2 x 32 = 8 + 8 + 48.
-constexpr int kLaRegsP = 88, kLaRegsV = 88, kLaRegsState = 128, kLaRegsIssue = 48;
-static_assert(kLaRegsP + kLaRegsV + 2 * kLaRegsState + kLaRegsIssue <= 5 * 96, "registers at launch");
+constexpr int kLaRegsOperands = 88, kLaRegsState = 128, kLaRegsIssue = 48;
+static_assert(2 * kLaRegsOperands + 2 * kLaRegsState + kLaRegsIssue <= 5 * 96, "registers at launch");
 constexpr uint32_t kLaTmemCols = 512;
 constexpr long long kLaWaitLimit = 4000000000LL;   // ~2 s of SM clocks per wait
 // The smallest log2 decay of a token: 2^-126 is the smallest normal fp32 number, so that a decay of
@@ -131,58 +131,102 @@ __device__ __forceinline__ LaItem la_item(const LaProblem &p, long long idx) {
   return it;
 }
 
-// S^T row v of (sequence s, head h), columns [k0, k0 + N): to and from the caller's state.
-template <int K, int V, int N>
-__device__ __forceinline__ void la_state_load(const LaProblem &p, int s, int h, int v, int k0, float (&S)[N]) {
+// S^T rows v0 + lane of (sequence s, head h), columns [k0, k0 + N), between a warp's registers and the
+// caller's state. In the [V, K] layout a thread's values are contiguous, but the warp's are 32 rows
+// apart: they change places in `buf`, 32 rows of K / 4 columns of shared memory that the warp has to
+// itself, so that every access covers whole 128-byte (64-byte) pieces of a row.
+template <int K, int V, int N, bool STORE>
+__device__ __forceinline__ void la_state_move(const LaProblem &p, int s, int h, int v0, int k0, float (&S)[N],
+                                              unsigned char *buf) {
+  const int lane = threadIdx.x & 31;
   const long long base = ((long long)s * p.H + h) * K * V;
-  if (p.flags & kStateKV) {
+  const bool bf16 = p.flags & kStateBf16;
+  const float *in32 = static_cast<const float *>(p.init) + base;
+  const __nv_bfloat16 *in16 = static_cast<const __nv_bfloat16 *>(p.init) + base;
+  float *out32 = static_cast<float *>(p.final_state) + base;
+  __nv_bfloat16 *out16 = static_cast<__nv_bfloat16 *>(p.final_state) + base;
+  if (p.flags & kStateKV) {   // a warp's values of one column are contiguous
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const long long i = base + (long long)(k0 + j) * V + v;
-      S[j] = (p.flags & kStateBf16) ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.init)[i])
-                                    : static_cast<const float *>(p.init)[i];
+      const int i = (k0 + j) * V + v0 + lane;
+      if (STORE && bf16) out16[i] = __float2bfloat16_rn(S[j]);
+      else if (STORE) out32[i] = S[j];
+      else S[j] = bf16 ? __bfloat162float(in16[i]) : in32[i];
     }
-  } else if (p.flags & kStateBf16) {
-    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.init) + base + (long long)v * K + k0);
+    return;
+  }
+  constexpr int kCols = K / 4;
+  uint4 *b4 = reinterpret_cast<uint4 *>(buf);
 #pragma unroll
-    for (int j = 0; j < N / 8; ++j) {
-      const uint4 r = src[j];
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  for (int r = 0; r < N; r += kCols) {
+    if (bf16) {
+      constexpr int kChunks = kCols / 8;   // 16-byte chunks of a row
+      uint4 *mine = b4 + lane * kChunks;
+      auto global = [&](int i) {           // row and chunk of this lane in step i of kChunks
+        const int row = i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
+        uint4 *at = b4 + row * kChunks + (c ^ (row & (kChunks - 1)));
+        const int g = (v0 + row) * K + k0 + r + c * 8;
+        if (STORE) *reinterpret_cast<uint4 *>(out16 + g) = *at;
+        else *at = *reinterpret_cast<const uint4 *>(in16 + g);
+      };
+      if (!STORE) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        S[8 * j + 2 * e] = __uint_as_float(w[e] << 16);
-        S[8 * j + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        for (int i = 0; i < kChunks; ++i) global(i);
+        __syncwarp();
+      }
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) {
+        uint4 &at = mine[j ^ (lane & (kChunks - 1))];
+        float *x = &S[r + 8 * j];
+        if (STORE) {
+          at = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        } else {
+          const uint4 w = at;
+          x[0] = __uint_as_float(w.x << 16); x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+          x[2] = __uint_as_float(w.y << 16); x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+          x[4] = __uint_as_float(w.z << 16); x[5] = __uint_as_float(w.z & 0xFFFF0000u);
+          x[6] = __uint_as_float(w.w << 16); x[7] = __uint_as_float(w.w & 0xFFFF0000u);
+        }
+      }
+      __syncwarp();
+      if (STORE) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) global(i);
+        __syncwarp();
+      }
+    } else {
+      constexpr int kChunks = kCols / 4;
+      uint4 *mine = b4 + lane * kChunks;
+      auto global = [&](int i) {
+        const int row = i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
+        uint4 *at = b4 + row * kChunks + (c ^ (row & (kChunks - 1)));
+        const int g = (v0 + row) * K + k0 + r + c * 4;
+        if (STORE) *reinterpret_cast<uint4 *>(out32 + g) = *at;
+        else *at = *reinterpret_cast<const uint4 *>(in32 + g);
+      };
+      if (!STORE) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) global(i);
+        __syncwarp();
+      }
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) {
+        uint4 &at = mine[j ^ (lane & (kChunks - 1))];
+        float *x = &S[r + 4 * j];
+        if (STORE) {
+          at = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        } else {
+          const uint4 w = at;
+          x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
+        }
+      }
+      __syncwarp();
+      if (STORE) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) global(i);
+        __syncwarp();
       }
     }
-  } else {
-    const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.init) + base + (long long)v * K + k0);
-#pragma unroll
-    for (int j = 0; j < N / 4; ++j) {
-      const float4 f = src[j];
-      S[4 * j] = f.x; S[4 * j + 1] = f.y; S[4 * j + 2] = f.z; S[4 * j + 3] = f.w;
-    }
-  }
-}
-template <int K, int V, int N>
-__device__ __forceinline__ void la_state_store(const LaProblem &p, int s, int h, int v, int k0, const float (&S)[N]) {
-  const long long base = ((long long)s * p.H + h) * K * V;
-  if (p.flags & kStateKV) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const long long i = base + (long long)(k0 + j) * V + v;
-      if (p.flags & kStateBf16) static_cast<__nv_bfloat16 *>(p.final_state)[i] = __float2bfloat16_rn(S[j]);
-      else static_cast<float *>(p.final_state)[i] = S[j];
-    }
-  } else if (p.flags & kStateBf16) {
-    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.final_state) + base + (long long)v * K + k0);
-#pragma unroll
-    for (int j = 0; j < N / 8; ++j)
-      dst[j] = make_uint4(pack_bf16(S[8 * j], S[8 * j + 1]), pack_bf16(S[8 * j + 2], S[8 * j + 3]),
-                          pack_bf16(S[8 * j + 4], S[8 * j + 5]), pack_bf16(S[8 * j + 6], S[8 * j + 7]));
-  } else {
-    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.final_state) + base + (long long)v * K + k0);
-#pragma unroll
-    for (int j = 0; j < N / 4; ++j) dst[j] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
   }
 }
 
@@ -219,8 +263,8 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
   }
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      umma::mbar_init(&ms.v_rdy[s], 4);
-      umma::mbar_init(&ms.v_read[s], 4);
+      umma::mbar_init(&ms.v_rdy[s], 8);
+      umma::mbar_init(&ms.v_read[s], 8);
       umma::mbar_init(&ms.full[s], 2);        // the loads' issuer and the factors' writer
       umma::mbar_init(&ms.empty[s], (AGG ? 1 : 2) + 8);   // M4, M3 and the eight state warps
       umma::mbar_init(&ms.full_v[s], 1);
@@ -232,7 +276,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
       umma::mbar_init(&ms.vp_free[b], 1);
     }
     umma::mbar_init(&ms.p_raw, 1);
-    umma::mbar_init(&ms.p_rdy, 4);
+    umma::mbar_init(&ms.p_rdy, 8);
     umma::mbar_init(&ms.s_free, 1);
     umma::mbar_init(&ms.o_done, 1);
     umma::mbar_init(&ms.o_free, 8);
@@ -300,9 +344,26 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
   if (warp == 16) {
     // ======================= loads and decay factors =======================
     const int hq_group = p.H / p.Hk;
+    const bool per_token = p.flags & kLaTokenDecay;
     int issued = 0, issued_v = 0;
-    for_chunks(nothing, [&](const LaItem &it, int h, int c, int, int n) {
-      const int st = (int)(n % kStages);
+    // Lane l: tokens 4 l .. 4 l + 3; lanes 8 c .. 8 c + 7 are 32-token block c. The decays of a chunk are
+    // loaded while the one before is in use. A full chunk's factors of a head without decays per token are
+    // those of any other: they stay in their stage (held: that head, by stage).
+    float next[4] = {0.f, 0.f, 0.f, 0.f};
+    int held[3] = {-1, -1, -1};
+    auto load_decays = [&](const LaItem &it, int h, int c) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = c * kLaChunk + 4 * lane + e;
+        if (i < it.len)
+          next[e] = per_token ? p.decay[it.b * p.ds[0] + (long long)(it.t0 + i) * p.ds[1] + h * p.ds[2]] : p.decay[h];
+      }
+    };
+    for_chunks([&](const LaItem &it, int h, int nch) {
+      if (nch > 0) load_decays(it, h, 0);
+      return true;
+    }, [&](const LaItem &it, int h, int c, int nch, int n) {
+      const int st = n % kStages;
       const uint32_t ph = (uint32_t)((n / kStages) & 1);
       if (n >= kStages && !wait(&ms.empty[st], ph ^ 1u)) return false;
       const int t0 = it.t0 + c * kLaChunk, L = min(kLaChunk, it.len - c * kLaChunk);
@@ -314,64 +375,67 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           for (int x = 0; x < K / 64; ++x) umma::tma_load_4d(dst + x * Lay::panel, &maps.q, x * 64, hq, t0, it.b, &ms.full[st]);
         for (int x = 0; x < K / 64; ++x) umma::tma_load_4d(dst + Lay::k_off + x * Lay::panel, &maps.k, x * 64, hq, t0, it.b, &ms.full[st]);
       }
-      // Lane l: tokens 4 l .. 4 l + 3; lanes 8 c .. 8 c + 7 are 32-token block c.
-      float a[4], pre[4], suf[4];
+      const int here = st == 0 ? held[0] : st == 1 ? held[1] : held[2];
+      if (per_token || L < kLaChunk || here != h) {
+        float a[4], pre[4], suf[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 4 * lane + e;
-        float x = 0.f;
-        if (i < L) {
-          x = (p.flags & kLaTokenDecay) ? p.decay[it.b * p.ds[0] + (long long)(t0 + i) * p.ds[1] + h * p.ds[2]] : p.decay[h];
-          x *= kLog2e;
-          x = x < kLaMinLog2 ? kLaMinLog2 : x;   // NaN stays
+        for (int e = 0; e < 4; ++e) {
+          const float x = next[e] * kLog2e;
+          a[e] = 4 * lane + e >= L ? 0.f : x < kLaMinLog2 ? kLaMinLog2 : x;   // NaN stays
         }
-        a[e] = x;
-      }
-      pre[0] = a[0];
-      suf[3] = 0.f;
+        if (c + 1 < nch) load_decays(it, h, c + 1);
+        pre[0] = a[0];
+        suf[3] = 0.f;
 #pragma unroll
-      for (int e = 1; e < 4; ++e) {
-        pre[e] = pre[e - 1] + a[e];
-        suf[3 - e] = suf[4 - e] + a[4 - e];
-      }
-      float incl = pre[3];   // sums through this lane
+        for (int e = 1; e < 4; ++e) {
+          pre[e] = pre[e - 1] + a[e];
+          suf[3 - e] = suf[4 - e] + a[4 - e];
+        }
+        float incl = pre[3];   // sums through this lane
 #pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const float y = __shfl_up_sync(0xffffffffu, incl, m);
-        if (lane >= m) incl += y;
-      }
-      float before = __shfl_up_sync(0xffffffffu, incl, 1);
-      if (lane == 0) before = 0.f;
-      // sums over the later lanes of the block, formed from the block's end so that small sums
-      // near the end keep their precision
-      float after = pre[3];
+        for (int m = 1; m < 32; m <<= 1) {
+          const float y = __shfl_up_sync(0xffffffffu, incl, m);
+          if (lane >= m) incl += y;
+        }
+        float before = __shfl_up_sync(0xffffffffu, incl, 1);
+        if (lane == 0) before = 0.f;
+        // sums over the later lanes of the block, formed from the block's end so that small sums
+        // near the end keep their precision
+        float after = pre[3];
 #pragma unroll
-      for (int m = 1; m < 8; m <<= 1) {
-        const float y = __shfl_down_sync(0xffffffffu, after, m);
-        if ((lane & 7) + m < 8) after += y;
-      }
-      const float block = __shfl_sync(0xffffffffu, after, lane & 24);   // the block's total
-      const float later = __shfl_down_sync(0xffffffffu, after, 1);
-      const float tail = (lane & 7) == 7 ? 0.f : later;
-      LaGate &g = gates[st];
-      const bool weak = __shfl_sync(0xffffffffu, incl, 31) >= kLaRowLog2;   // so are all sums, for decays <= 1
+        for (int m = 1; m < 8; m <<= 1) {
+          const float y = __shfl_down_sync(0xffffffffu, after, m);
+          if ((lane & 7) + m < 8) after += y;
+        }
+        const float block = __shfl_sync(0xffffffffu, after, lane & 24);   // the block's total
+        const float later = __shfl_down_sync(0xffffffffu, after, 1);
+        const float tail = (lane & 7) == 7 ? 0.f : later;
+        LaGate &g = gates[st];
+        const bool weak = __shfl_sync(0xffffffffu, incl, 31) >= kLaRowLog2;   // so are all sums, for decays <= 1
+        float G[4], cf[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 4 * lane + e;
-        g.G[i] = weak ? ex2_approx(-(before + pre[e])) : before + pre[e];
-        g.cf[i] = i < L ? ex2_approx(suf[e] + tail) : 0.f;
+        for (int e = 0; e < 4; ++e) {
+          G[e] = weak ? ex2_approx(-(before + pre[e])) : before + pre[e];
+          cf[e] = 4 * lane + e < L ? ex2_approx(suf[e] + tail) : 0.f;
+        }
+        *reinterpret_cast<float4 *>(&g.G[4 * lane]) = make_float4(G[0], G[1], G[2], G[3]);
+        *reinterpret_cast<float4 *>(&g.cf[4 * lane]) = make_float4(cf[0], cf[1], cf[2], cf[3]);
+        const float b1 = __shfl_sync(0xffffffffu, block, 8), b2 = __shfl_sync(0xffffffffu, block, 16),
+                    b3 = __shfl_sync(0xffffffffu, block, 24), b0 = __shfl_sync(0xffffffffu, block, 0);
+        if (lane == 0) {
+          g.bf[0] = ex2_approx(b1 + b2 + b3);
+          g.bf[1] = ex2_approx(b2 + b3);
+          g.bf[2] = ex2_approx(b3);
+          g.bf[3] = 1.f;
+          g.gamma = ex2_approx(b0 + b1 + b2 + b3);
+          g.weak = weak;
+        }
+        __syncwarp();
+        const int keep = per_token || L < kLaChunk ? -1 : h;
+        if (st == 0) held[0] = keep;
+        else if (st == 1) held[1] = keep;
+        else held[2] = keep;
       }
-      const float b1 = __shfl_sync(0xffffffffu, block, 8), b2 = __shfl_sync(0xffffffffu, block, 16),
-                  b3 = __shfl_sync(0xffffffffu, block, 24), b0 = __shfl_sync(0xffffffffu, block, 0);
-      if (lane == 0) {
-        g.bf[0] = ex2_approx(b1 + b2 + b3);
-        g.bf[1] = ex2_approx(b2 + b3);
-        g.bf[2] = ex2_approx(b3);
-        g.bf[3] = 1.f;
-        g.gamma = ex2_approx(b0 + b1 + b2 + b3);
-        g.weak = weak;
-      }
-      __syncwarp();
       if (lane == 0) umma::mbar_arrive(&ms.full[st]);
       issued = n + 1;
       if (n >= kStages && !wait(&ms.empty_v[st], ph ^ 1u)) return false;
@@ -492,68 +556,27 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
         return true;
       }, nothing);
     }
-  } else if (warp < 4) {
-    // ======================= P =======================
-    umma::regs_dec<kLaRegsP>();
-    if constexpr (!AGG) {
-      for_chunks(nothing, [&](const LaItem &, int, int, int, int n) {
-        const int st = (int)(n % kStages);
-        if (!wait(&ms.full[st], (uint32_t)((n / kStages) & 1))) return false;
-        const LaGate &g = gates[st];
-        const bool weak = g.weak != 0;
-        const float Gr = weak ? 0.f : g.G[row] - fmaxf(g.G[row], kLaRowLog2);   // G_i - R_i
-        if (!wait(&ms.p_raw, (uint32_t)(n & 1))) return false;
-        // Rolled over 32-column blocks: a warp runs its role alone on its scheduler, and code that does not
-        // repeat is fetched at every step (unrolled, with loads a block ahead, P took twice as long).
-#pragma unroll 1
-        for (int c = 0; c <= warp; ++c) {
-          float x[32];
-          umma::tmem_ld32(tmem + kTmP + lane_base + c * 32, x);
-          umma::tmem_ld_wait();
-          if (weak) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 w = *reinterpret_cast<const float4 *>(&g.G[32 * c + j]);
-              const float2 a = __fmul2_rn(make_float2(x[j], x[j + 1]), make_float2(w.x, w.y));
-              const float2 b = __fmul2_rn(make_float2(x[j + 2], x[j + 3]), make_float2(w.z, w.w));
-              x[j] = a.x; x[j + 1] = a.y; x[j + 2] = b.x; x[j + 3] = b.y;
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] *= ex2_approx(Gr - g.G[32 * c + j]);
-          }
-          if (c == warp) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
-          }
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-          umma::tmem_st16(tmem + kTmP + lane_base + c * 16, pk);
-        }
-#pragma unroll 1
-        for (int c = 2 * warp + 2; c < 8; ++c) {
-          const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-          umma::tmem_st8(tmem + kTmP + lane_base + c * 8, zero);
-        }
-        umma::tmem_st_wait();
-        arrive(&ms.p_rdy);
-        return true;
-      }, nothing);
-    }
   } else if (warp < 8) {
-    // ======================= V' =======================
-    umma::regs_dec<kLaRegsV>();
+    // ======================= P and V' =======================
+    umma::regs_dec<kLaRegsOperands>();
+    const int wg = warp >> 2, quad = warp & 3;
+    const bool has_ch = quad * 32 < V;   // V' lanes are value columns
+    // 8 x 8 blocks of the v tile, transposed: matrix i of a load is channels 8 (i % 2), tokens 8 (i / 2) of
+    // 16 channels x 16 tokens; lane l names token l % 8 of matrix l / 8
+    const int ch0 = quad * 32 + ((lane >> 3) & 1) * 8;
+    const uint32_t v_src = (uint32_t)((ch0 >> 6) * Lay::panel + ((lane >> 4) * 8 + (lane & 7)) * 128);
+    // The roles' loops stay rolled: each warp runs alone on its scheduler in its role, and code that does
+    // not repeat is fetched at every step (fully unrolled, P and V' took twice as long).
     for_chunks(nothing, [&](const LaItem &it, int, int c, int, int n) {
-      const int st = (int)(n % kStages);
-      if (!wait(&ms.full[st], (uint32_t)((n / kStages) & 1)) || !wait(&ms.full_v[st], (uint32_t)((n / kStages) & 1)))
-        return false;
+      const int st = n % kStages;
+      const uint32_t sph = (uint32_t)((n / kStages) & 1);
+      if (!wait(&ms.full[st], sph) || !wait(&ms.full_v[st], sph)) return false;
       unsigned char *kt = sm + st * Lay::stage + Lay::k_off, *vt = sm + st * Lay::stage + Lay::v_off;
       const int L = min(kLaChunk, it.len - c * kLaChunk);
       if (L < kLaChunk) {
         // k and v rows past the sequence hold the next packed sequence: their factors are zero, but
         // zero times an inf or NaN there would not be
-        for (int x = tid - 128; x < (kLaChunk - L) * 8; x += 128) {
+        for (int x = tid; x < (kLaChunk - L) * 8; x += 256) {
           const uint32_t off = (uint32_t)(L * 128 + x * 16);
 #pragma unroll
           for (int y = 0; y < K / 64; ++y) *reinterpret_cast<uint4 *>(kt + y * Lay::panel + off) = make_uint4(0, 0, 0, 0);
@@ -561,62 +584,101 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           for (int y = 0; y < V / 64; ++y) *reinterpret_cast<uint4 *>(vt + y * Lay::panel + off) = make_uint4(0, 0, 0, 0);
         }
         umma::fence_proxy_async_smem();
-        umma::named_bar(1, 128);
+        umma::named_bar(1, 256);
       }
       if constexpr (!AGG) arrive(&ms.v_rdy[st]);
       const LaGate &g = gates[st];
-      // 8 x 8 blocks of the tile, transposed: matrix i of a load is channels 8 (i % 2), tokens 8 (i / 2) of
-      // this warp's 16 channels x 16 tokens; lane l names token l % 8 of matrix l / 8
-      const int ch0 = (warp & 3) * 32 + ((lane >> 3) & 1) * 8;
-      const uint32_t src = umma::smem_u32(vt) + (ch0 >> 6) * Lay::panel + ((lane >> 4) * 8 + (lane & 7)) * 128;
-      uint32_t raw[16];   // of 32 tokens: [16 channels][8-token block][8 channels]
-      auto load = [&](int b) {
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            umma::ldmatrix_x4_trans(src + (32 * b + 16 * i) * 128 + (uint32_t)(((((ch0 & 63) >> 3) + 2 * hh) ^ (lane & 7)) << 4),
-                                    raw[8 * hh + 4 * i], raw[8 * hh + 4 * i + 1], raw[8 * hh + 4 * i + 2], raw[8 * hh + 4 * i + 3]);
-      };
-      const bool has_ch = (warp & 3) * 32 < V;
-      if (has_ch) load(0);
 #pragma unroll 1
-      for (int b = 0; b < 4; ++b) {
-        const int buf = b & 1;
-        uint32_t t0[16], t1[16], t2[16];
-        if (has_ch) {
-          const float bf = g.bf[b];
-          const float2 minus = make_float2(-1.f, -1.f);
+      for (int part = 0; part < 3; ++part) {
+        if (part != 1) {
+          // ---- V' of 32 tokens, block b = wg or wg + 2
+          const int b = wg + part;
+          uint32_t t0[16], t1[16], t2[16];   // the three terms, [16 channels][8-token block][8 channels]
+          if (has_ch) {
+            uint32_t raw[16];
+            const uint32_t src = umma::smem_u32(vt) + v_src + (uint32_t)(32 * b * 128);
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {   // factors of tokens 8 m + 2 (l % 4) and the next
-            const float2 w = __fmul2_rn(*reinterpret_cast<const float2 *>(&g.cf[32 * b + 8 * m + 2 * (lane & 3)]), make_float2(bf, bf));
+            for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {   // token pairs of channels 16 (e / 2) + 8 (e % 2)
-              const int r = 8 * (e >> 1) + 2 * m + (e & 1);
-              float2 x = __fmul2_rn(make_float2(__uint_as_float(raw[r] << 16), __uint_as_float(raw[r] & 0xFFFF0000u)), w);
-              t0[r] = pack_bf16(x.x, x.y);
-              x = __ffma2_rn(make_float2(__uint_as_float(t0[r] << 16), __uint_as_float(t0[r] & 0xFFFF0000u)), minus, x);
-              t1[r] = pack_bf16(x.x, x.y);
-              x = __ffma2_rn(make_float2(__uint_as_float(t1[r] << 16), __uint_as_float(t1[r] & 0xFFFF0000u)), minus, x);
-              t2[r] = pack_bf16(x.x, x.y);
+              for (int i = 0; i < 2; ++i)
+                umma::ldmatrix_x4_trans(src + 16 * i * 128 + (uint32_t)(((((ch0 & 63) >> 3) + 2 * hh) ^ (lane & 7)) << 4),
+                                        raw[8 * hh + 4 * i], raw[8 * hh + 4 * i + 1], raw[8 * hh + 4 * i + 2], raw[8 * hh + 4 * i + 3]);
+            const float bf = g.bf[b];
+            const float2 minus = make_float2(-1.f, -1.f);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {   // factors of tokens 8 m + 2 (l % 4) and the next
+              const float2 w = __fmul2_rn(*reinterpret_cast<const float2 *>(&g.cf[32 * b + 8 * m + 2 * (lane & 3)]), make_float2(bf, bf));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {   // token pairs of channels 16 (e / 2) + 8 (e % 2)
+                const int r = 8 * (e >> 1) + 2 * m + (e & 1);
+                float2 x = __fmul2_rn(make_float2(__uint_as_float(raw[r] << 16), __uint_as_float(raw[r] & 0xFFFF0000u)), w);
+                t0[r] = pack_bf16(x.x, x.y);
+                x = __ffma2_rn(make_float2(__uint_as_float(t0[r] << 16), __uint_as_float(t0[r] & 0xFFFF0000u)), minus, x);
+                t1[r] = pack_bf16(x.x, x.y);
+                x = __ffma2_rn(make_float2(__uint_as_float(t1[r] << 16), __uint_as_float(t1[r] & 0xFFFF0000u)), minus, x);
+                t2[r] = pack_bf16(x.x, x.y);
+              }
             }
           }
-          if (b < 3) load(b + 1);
-        }
-        if (b == 3 && !AGG) arrive(&ms.v_read[st]);
-        // M4 has read the buffer's last content (two phases per chunk: the one before this is b / 2 - 1)
-        if ((n > 0 || b >= 2) && !wait(&ms.vp_free[buf], (uint32_t)((b >> 1) ^ 1))) return false;
-        if (has_ch) {
+          if (!AGG && part == 2) arrive(&ms.v_read[st]);
+          // M4 has read the buffer's last content (two phases per chunk: the one before this is part / 2 - 1)
+          if ((n > 0 || part) && !wait(&ms.vp_free[wg], (uint32_t)((part >> 1) ^ 1))) return false;
+          if (has_ch) {
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {   // 16 channels each
-            const uint32_t dst = tmem + kTmVp + buf * kTmVpBuf + lane_base + ((uint32_t)(hh * 16) << 16);
-            umma::tmem_st_16x128b_x4(dst, t0 + 8 * hh);
-            umma::tmem_st_16x128b_x4(dst + 16, t1 + 8 * hh);
-            umma::tmem_st_16x128b_x4(dst + 32, t2 + 8 * hh);
+            for (int hh = 0; hh < 2; ++hh) {   // 16 channels each
+              const uint32_t dst = tmem + kTmVp + wg * kTmVpBuf + lane_base + ((uint32_t)(hh * 16) << 16);
+              umma::tmem_st_16x128b_x4(dst, t0 + 8 * hh);
+              umma::tmem_st_16x128b_x4(dst + 16, t1 + 8 * hh);
+              umma::tmem_st_16x128b_x4(dst + 32, t2 + 8 * hh);
+            }
+            umma::tmem_st_wait();
+          }
+          arrive(&ms.vp_rdy[wg]);
+        } else if (!AGG) {
+          // ---- P: columns 32 c2 .. of blocks c2 = wg, wg + 2
+          const bool weak = g.weak != 0;
+          const float Gr = weak ? 0.f : g.G[row] - fmaxf(g.G[row], kLaRowLog2);   // G_i - R_i
+          if (!wait(&ms.p_raw, (uint32_t)(n & 1))) return false;
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            const int c2 = wg + 2 * i;
+            float x[32];
+            uint32_t pk[16];
+            if (c2 <= quad) {
+              umma::tmem_ld32(tmem + kTmP + lane_base + c2 * 32, x);
+              umma::tmem_ld_wait();
+            }
+            // P's columns 0-31 take the place of the scores' first block, read by warpgroup 0, columns 32-63
+            // that of the second, read by warpgroup 1: both have been read past this point
+            if (i == 0) umma::named_bar(2 + quad, 64);
+            if (c2 <= quad) {
+              if (weak) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                  const float4 w = *reinterpret_cast<const float4 *>(&g.G[32 * c2 + j]);
+                  const float2 a = __fmul2_rn(make_float2(x[j], x[j + 1]), make_float2(w.x, w.y));
+                  const float2 b = __fmul2_rn(make_float2(x[j + 2], x[j + 3]), make_float2(w.z, w.w));
+                  x[j] = a.x; x[j + 1] = a.y; x[j + 2] = b.x; x[j + 3] = b.y;
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] *= ex2_approx(Gr - g.G[32 * c2 + j]);
+              }
+              if (c2 == quad) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) pk[j] = 0u;
+            }
+            umma::tmem_st16(tmem + kTmP + lane_base + c2 * 16, pk);
           }
           umma::tmem_st_wait();
+          arrive(&ms.p_rdy);
         }
-        arrive(&ms.vp_rdy[buf]);
       }
       return true;
     }, nothing);
@@ -637,6 +699,8 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
                        pack_bf16(S[j + 6], S[j + 7]));
       }
     };
+    // this warp's part of the copy's buffer, for the states' way to and from memory between items
+    unsigned char *patch = sm + Lay::s_off + (half * (V / 32) + (warp & 3)) * (32 * (K / 4) * 4);
     auto seg_block = [&](int slot, int h) { return p.seg_state + ((long long)slot * p.H + h) * (K * V); };
     for_chunks(
         [&](const LaItem &it, int h, int nch) {
@@ -644,7 +708,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
 #pragma unroll
             for (int j = 0; j < KH; ++j) S[j] = 0.f;
           } else if (it.seg == 0) {
-            la_state_load<K, V>(p, it.seq, h, row, half * KH, S);
+            la_state_move<K, V, KH, false>(p, it.seq, h, (warp & 3) * 32, half * KH, S, patch);
           } else {
             const float *src = seg_block(it.slot - 1, h);
 #pragma unroll
@@ -654,6 +718,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
             }
           }
           seg_decay = 1.f;
+          if constexpr (!AGG) umma::named_bar(6, 256);   // all patches of the copy's buffer are done with
           if (!AGG && nch > 0) {   // M2 of the item before has read its copy (s_free)
             if (has_v) {
 #pragma unroll
@@ -685,6 +750,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
                 float y[32];
                 umma::tmem_ld32(tmem + kTmD + lane_base + half * KH + x, y);
                 umma::tmem_ld_wait();
+                if (x + 32 >= KH) arrive(&ms.d_free);
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
                   const float2 a = __ffma2_rn(make_float2(gamma, gamma), make_float2(S[x + j], S[x + j + 1]), make_float2(y[j], y[j + 1]));
@@ -693,8 +759,9 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
                 }
                 if (copy) copy_s(x);
               }
+            } else {
+              arrive(&ms.d_free);
             }
-            arrive(&ms.d_free);
             if constexpr (AGG) seg_decay *= gamma;
             if (copy) {
               umma::fence_proxy_async_smem();
@@ -710,6 +777,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
               float y[32];
               umma::tmem_ld32(tmem + kTmO + lane_base + half * VH + x, y);
               umma::tmem_ld_wait();
+              if (x + 32 >= VH) arrive(&ms.o_free);
               const int col = half * VH + x;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
@@ -723,7 +791,6 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
                     make_uint4(pk[0], pk[1], pk[2], pk[3]);
               }
             }
-            arrive(&ms.o_free);
             umma::fence_proxy_async_smem();
             arrive(&ms.o_st[st]);
             return true;
@@ -746,7 +813,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
                   make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
             if (tid == 8 * 32) p.seg_decay[(long long)it.slot * p.H + h] = seg_decay;
           } else if (it.seg == it.n_seg - 1 && p.final_state) {
-            la_state_store<K, V>(p, it.seq, h, row, half * KH, S);
+            la_state_move<K, V, KH, true>(p, it.seq, h, (warp & 3) * 32, half * KH, S, patch);
           }
           return true;
         });
