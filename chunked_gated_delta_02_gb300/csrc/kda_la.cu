@@ -27,9 +27,9 @@
 // A CTA takes (sequence segment, head) items, all V columns at once, so that q, k and v are read
 // once; it is persistent over items (one CTA per SM: two stages of q, k and v and S fill the
 // shared memory). Warp roles, coupled by mbarriers only:
-//   warps 0-7    P, in place of the scores in tensor memory (A operand of M3), each warpgroup every
-//                other 32 columns; V', transposed from the v tile into tensor memory (A operand of
-//                M4), each warpgroup every other 32 tokens, with a buffer of its own
+//   warps 0-3    P, in place of the scores in tensor memory (A operand of M3)
+//   warps 4-7    V', transposed from the v tile into tensor memory (A operand of M4), 32 tokens at
+//                a time into two buffers in turn
 //   warps 8-15   the state, and the scaled output in bf16
 //   warp 16      loads (TMA, 128-byte swizzle) and the chunk's decay factors
 //   warp 17      issues M1, M2 and M3;  warp 18  issues M4
@@ -39,7 +39,10 @@
 //
 // Bound: a chunk of one head moves 128 KiB at K = V = 128, 2.9 us of an SM's share of the measured
 // bandwidth, against 48 tensor-core steps of 64 clocks, 1.6 us: memory bandwidth, if loads, products
-// and register work overlap.
+// and register work overlap. Shared memory holds two chunks, so a chunk's period is half the time from
+// the request of its tiles to their release: that time is kept short by forming V' and P in separate
+// warps and by releasing q, k and v on their own. (o leaves by the copy engine: stored by the state warps
+// it took 1400 clocks of their time from shared memory and 2700 from registers.)
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -77,11 +80,12 @@ struct LaGate {
 };
 
 struct LaMisc {
-  // per stage: q, k and the decay factors ready and consumed; the same of v, whose buffer then holds
-  // the output tile; v rows past the sequence cleared; V' formed; output tile written
-  uint64_t full[3], empty[3], full_v[3], empty_v[3], v_rdy[3], v_read[3], o_st[3];
+  // per stage: q and k loaded, consumed; v loaded, consumed; decay factors written (consumed with q and
+  // k); v rows past the sequence cleared; V' formed; output tile written over v
+  uint64_t full[3], empty[3], full_v[3], empty_v[3], gate[3], v_rdy[3], v_read[3], o_st[3];
   uint64_t p_raw, p_rdy, s_free, o_done, o_free, d_rdy, d_free, s_rdy;   // one phase per chunk
   uint64_t vp_rdy[2], vp_free[2];                   // per V' buffer: 32 tokens ready, read
+  uint64_t state_sync;                              // the state warps among themselves
   uint64_t bar_exit;
   uint32_t tmem_slot;
   int err;
@@ -93,7 +97,7 @@ struct LaLayout {
   static constexpr uint32_t k_off = AGG ? 0 : (K / 64) * panel;
   static constexpr uint32_t v_off = k_off + (K / 64) * panel;
   static constexpr uint32_t stage = v_off + (V / 64) * panel;
-  static constexpr int stages = AGG ? 3 : 2;
+  static constexpr int stages = (AGG || K + V == 128) ? 3 : 2;
   static constexpr uint32_t s_off = stages * stage;                 // S^T rows v, bf16, K-major panels
   static constexpr uint32_t s_panel = V * 128;
   static constexpr uint32_t gate = s_off + (AGG ? 0 : (K / 64) * s_panel);
@@ -263,12 +267,13 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
   }
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      umma::mbar_init(&ms.v_rdy[s], 8);
-      umma::mbar_init(&ms.v_read[s], 8);
-      umma::mbar_init(&ms.full[s], 2);        // the loads' issuer and the factors' writer
-      umma::mbar_init(&ms.empty[s], (AGG ? 1 : 2) + 8);   // M4, M3 and the eight state warps
+      umma::mbar_init(&ms.full[s], 1);
       umma::mbar_init(&ms.full_v[s], 1);
-      umma::mbar_init(&ms.empty_v[s], 1);
+      umma::mbar_init(&ms.gate[s], 1);
+      umma::mbar_init(&ms.v_rdy[s], 4);
+      umma::mbar_init(&ms.empty[s], AGG ? 1 + 8 : 2 + 4 + 8);   // M4, M2, P and state warps
+      umma::mbar_init(&ms.empty_v[s], AGG ? 8 : 1);             // V' warps; the output's store
+      umma::mbar_init(&ms.v_read[s], 4);
       umma::mbar_init(&ms.o_st[s], 8);
     }
     for (int b = 0; b < 2; ++b) {
@@ -276,10 +281,11 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
       umma::mbar_init(&ms.vp_free[b], 1);
     }
     umma::mbar_init(&ms.p_raw, 1);
-    umma::mbar_init(&ms.p_rdy, 8);
+    umma::mbar_init(&ms.p_rdy, 4);
     umma::mbar_init(&ms.s_free, 1);
     umma::mbar_init(&ms.o_done, 1);
     umma::mbar_init(&ms.o_free, 8);
+    umma::mbar_init(&ms.state_sync, 8);
     umma::mbar_init(&ms.d_rdy, 1);
     umma::mbar_init(&ms.d_free, 8);
     umma::mbar_init(&ms.s_rdy, 8);
@@ -375,6 +381,14 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           for (int x = 0; x < K / 64; ++x) umma::tma_load_4d(dst + x * Lay::panel, &maps.q, x * 64, hq, t0, it.b, &ms.full[st]);
         for (int x = 0; x < K / 64; ++x) umma::tma_load_4d(dst + Lay::k_off + x * Lay::panel, &maps.k, x * 64, hq, t0, it.b, &ms.full[st]);
       }
+      issued = n + 1;
+      if (n >= kStages && !wait(&ms.empty_v[st], ph ^ 1u)) return false;
+      if (umma::elect_one()) {
+        umma::mbar_arrive_expect_tx(&ms.full_v[st], Lay::stage - Lay::v_off);
+        for (int x = 0; x < V / 64; ++x)
+          umma::tma_load_4d(sm + st * Lay::stage + Lay::v_off + x * Lay::panel, &maps.v, x * 64, h, t0, it.b, &ms.full_v[st]);
+      }
+      issued_v = n + 1;
       const int here = st == 0 ? held[0] : st == 1 ? held[1] : held[2];
       if (per_token || L < kLaChunk || here != h) {
         float a[4], pre[4], suf[4];
@@ -436,15 +450,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
         else if (st == 1) held[1] = keep;
         else held[2] = keep;
       }
-      if (lane == 0) umma::mbar_arrive(&ms.full[st]);
-      issued = n + 1;
-      if (n >= kStages && !wait(&ms.empty_v[st], ph ^ 1u)) return false;
-      if (umma::elect_one()) {
-        umma::mbar_arrive_expect_tx(&ms.full_v[st], Lay::stage - Lay::v_off);
-        for (int x = 0; x < V / 64; ++x)
-          umma::tma_load_4d(sm + st * Lay::stage + Lay::v_off + x * Lay::panel, &maps.v, x * 64, h, t0, it.b, &ms.full_v[st]);
-      }
-      issued_v = n + 1;
+      if (lane == 0) umma::mbar_arrive(&ms.gate[st]);
       return true;
     }, nothing);
     // after a timeout: wait (bounded) for the copies in flight
@@ -484,6 +490,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
             umma::mma_f16_ss(tmem + kTmO, umma::desc_add(aq, (x / 4) * Lay::panel + (x % 4) * 32),
                              umma::desc_add(bs, (x / 4) * Lay::s_panel + (x % 4) * 32), id2, x > 0);
           umma::commit(&ms.s_free);
+          umma::commit(&ms.empty[st]);
         }
         // M3: O += P V; v_rdy: rows of the v tile past the sequence have been cleared
         if (!wait(&ms.v_rdy[st], sph) || !wait(&ms.p_rdy, ph)) return false;
@@ -492,7 +499,6 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           for (int x = 0; x < 8; ++x)
             umma::mma_f16_ts(tmem + kTmO, tmem + kTmP + x * 8, umma::desc_add(bv, x * 2048), id3, 1);
           umma::commit(&ms.o_done);
-          umma::commit(&ms.empty[st]);
         }
         __syncwarp();
         return true;
@@ -520,7 +526,6 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           if (b == 3) {
             umma::commit(&ms.d_rdy);
             umma::commit(&ms.empty[st]);
-            if constexpr (AGG) umma::commit(&ms.empty_v[st]);
           }
         }
         __syncwarp();
@@ -545,6 +550,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           }
         } else {                        // the rows after it are the next packed sequence's
           __nv_bfloat16 *dst = p.o + (((long long)it.b * p.T + t0) * p.H + h) * V;
+#pragma unroll 4
           for (int x = lane; x < L * (V / 8); x += 32) {
             const int i = x / (V / 8), j = x % (V / 8);
             *reinterpret_cast<uint4 *>(dst + (long long)i * p.H * V + j * 8) =
@@ -565,18 +571,22 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
     // 16 channels x 16 tokens; lane l names token l % 8 of matrix l / 8
     const int ch0 = quad * 32 + ((lane >> 3) & 1) * 8;
     const uint32_t v_src = (uint32_t)((ch0 >> 6) * Lay::panel + ((lane >> 4) * 8 + (lane & 7)) * 128);
+    // Without P to form, both warpgroups take every other 32 tokens of V', with a buffer of their own.
+    const int b_first = AGG ? wg : 0, b_step = AGG ? 2 : 1;
     // The roles' loops stay rolled: each warp runs alone on its scheduler in its role, and code that does
     // not repeat is fetched at every step (fully unrolled, P and V' took twice as long).
-    for_chunks(nothing, [&](const LaItem &it, int, int c, int, int n) {
+    if (AGG || wg == 1) for_chunks(nothing, [&](const LaItem &it, int, int c, int, int n) {
       const int st = n % kStages;
       const uint32_t sph = (uint32_t)((n / kStages) & 1);
-      if (!wait(&ms.full[st], sph) || !wait(&ms.full_v[st], sph)) return false;
+      if (!wait(&ms.full_v[st], sph) || !wait(&ms.gate[st], sph)) return false;
       unsigned char *kt = sm + st * Lay::stage + Lay::k_off, *vt = sm + st * Lay::stage + Lay::v_off;
       const int L = min(kLaChunk, it.len - c * kLaChunk);
       if (L < kLaChunk) {
         // k and v rows past the sequence hold the next packed sequence: their factors are zero, but
-        // zero times an inf or NaN there would not be
-        for (int x = tid; x < (kLaChunk - L) * 8; x += 256) {
+        // zero times an inf or NaN there would not be. This warpgroup clears them; what it reads
+        // below of v before that is masked.
+        if (!wait(&ms.full[st], sph)) return false;
+        for (int x = tid & 127; x < (kLaChunk - L) * 8; x += 128) {
           const uint32_t off = (uint32_t)(L * 128 + x * 16);
 #pragma unroll
           for (int y = 0; y < K / 64; ++y) *reinterpret_cast<uint4 *>(kt + y * Lay::panel + off) = make_uint4(0, 0, 0, 0);
@@ -584,102 +594,105 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           for (int y = 0; y < V / 64; ++y) *reinterpret_cast<uint4 *>(vt + y * Lay::panel + off) = make_uint4(0, 0, 0, 0);
         }
         umma::fence_proxy_async_smem();
-        umma::named_bar(1, 256);
       }
       if constexpr (!AGG) arrive(&ms.v_rdy[st]);
       const LaGate &g = gates[st];
 #pragma unroll 1
-      for (int part = 0; part < 3; ++part) {
-        if (part != 1) {
-          // ---- V' of 32 tokens, block b = wg or wg + 2
-          const int b = wg + part;
-          uint32_t t0[16], t1[16], t2[16];   // the three terms, [16 channels][8-token block][8 channels]
-          if (has_ch) {
-            uint32_t raw[16];
-            const uint32_t src = umma::smem_u32(vt) + v_src + (uint32_t)(32 * b * 128);
+      for (int b = b_first; b < 4; b += b_step) {
+        const int buf = b & 1;
+        uint32_t t0[16], t1[16], t2[16];   // the three terms, [16 channels][8-token block][8 channels]
+        if (has_ch) {
+          uint32_t raw[16];
+          const uint32_t src = umma::smem_u32(vt) + v_src + (uint32_t)(32 * b * 128);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
+          for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                umma::ldmatrix_x4_trans(src + 16 * i * 128 + (uint32_t)(((((ch0 & 63) >> 3) + 2 * hh) ^ (lane & 7)) << 4),
-                                        raw[8 * hh + 4 * i], raw[8 * hh + 4 * i + 1], raw[8 * hh + 4 * i + 2], raw[8 * hh + 4 * i + 3]);
-            const float bf = g.bf[b];
-            const float2 minus = make_float2(-1.f, -1.f);
+            for (int i = 0; i < 2; ++i)
+              umma::ldmatrix_x4_trans(src + 16 * i * 128 + (uint32_t)(((((ch0 & 63) >> 3) + 2 * hh) ^ (lane & 7)) << 4),
+                                      raw[8 * hh + 4 * i], raw[8 * hh + 4 * i + 1], raw[8 * hh + 4 * i + 2], raw[8 * hh + 4 * i + 3]);
+          if (L < kLaChunk) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {   // factors of tokens 8 m + 2 (l % 4) and the next
-              const float2 w = __fmul2_rn(*reinterpret_cast<const float2 *>(&g.cf[32 * b + 8 * m + 2 * (lane & 3)]), make_float2(bf, bf));
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {   // token pairs of channels 16 (e / 2) + 8 (e % 2)
-                const int r = 8 * (e >> 1) + 2 * m + (e & 1);
-                float2 x = __fmul2_rn(make_float2(__uint_as_float(raw[r] << 16), __uint_as_float(raw[r] & 0xFFFF0000u)), w);
-                t0[r] = pack_bf16(x.x, x.y);
-                x = __ffma2_rn(make_float2(__uint_as_float(t0[r] << 16), __uint_as_float(t0[r] & 0xFFFF0000u)), minus, x);
-                t1[r] = pack_bf16(x.x, x.y);
-                x = __ffma2_rn(make_float2(__uint_as_float(t1[r] << 16), __uint_as_float(t1[r] & 0xFFFF0000u)), minus, x);
-                t2[r] = pack_bf16(x.x, x.y);
-              }
+            for (int r = 0; r < 16; ++r) {   // tokens t and t + 1 of a pair
+              const int t = 32 * b + 8 * ((r >> 1) & 3) + 2 * (lane & 3);
+              raw[r] &= t + 1 < L ? 0xFFFFFFFFu : t < L ? 0xFFFFu : 0u;
             }
           }
-          if (!AGG && part == 2) arrive(&ms.v_read[st]);
-          // M4 has read the buffer's last content (two phases per chunk: the one before this is part / 2 - 1)
-          if ((n > 0 || part) && !wait(&ms.vp_free[wg], (uint32_t)((part >> 1) ^ 1))) return false;
-          if (has_ch) {
+          const float bf = g.bf[b];
+          const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {   // 16 channels each
-              const uint32_t dst = tmem + kTmVp + wg * kTmVpBuf + lane_base + ((uint32_t)(hh * 16) << 16);
-              umma::tmem_st_16x128b_x4(dst, t0 + 8 * hh);
-              umma::tmem_st_16x128b_x4(dst + 16, t1 + 8 * hh);
-              umma::tmem_st_16x128b_x4(dst + 32, t2 + 8 * hh);
+          for (int m = 0; m < 4; ++m) {   // factors of tokens 8 m + 2 (l % 4) and the next
+            const float2 w = __fmul2_rn(*reinterpret_cast<const float2 *>(&g.cf[32 * b + 8 * m + 2 * (lane & 3)]), make_float2(bf, bf));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {   // token pairs of channels 16 (e / 2) + 8 (e % 2)
+              const int r = 8 * (e >> 1) + 2 * m + (e & 1);
+              float2 x = __fmul2_rn(make_float2(__uint_as_float(raw[r] << 16), __uint_as_float(raw[r] & 0xFFFF0000u)), w);
+              t0[r] = pack_bf16(x.x, x.y);
+              x = __ffma2_rn(make_float2(__uint_as_float(t0[r] << 16), __uint_as_float(t0[r] & 0xFFFF0000u)), minus, x);
+              t1[r] = pack_bf16(x.x, x.y);
+              x = __ffma2_rn(make_float2(__uint_as_float(t1[r] << 16), __uint_as_float(t1[r] & 0xFFFF0000u)), minus, x);
+              t2[r] = pack_bf16(x.x, x.y);
             }
-            umma::tmem_st_wait();
           }
-          arrive(&ms.vp_rdy[wg]);
-        } else if (!AGG) {
-          // ---- P: columns 32 c2 .. of blocks c2 = wg, wg + 2
-          const bool weak = g.weak != 0;
-          const float Gr = weak ? 0.f : g.G[row] - fmaxf(g.G[row], kLaRowLog2);   // G_i - R_i
-          if (!wait(&ms.p_raw, (uint32_t)(n & 1))) return false;
-#pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            const int c2 = wg + 2 * i;
-            float x[32];
-            uint32_t pk[16];
-            if (c2 <= quad) {
-              umma::tmem_ld32(tmem + kTmP + lane_base + c2 * 32, x);
-              umma::tmem_ld_wait();
-            }
-            // P's columns 0-31 take the place of the scores' first block, read by warpgroup 0, columns 32-63
-            // that of the second, read by warpgroup 1: both have been read past this point
-            if (i == 0) umma::named_bar(2 + quad, 64);
-            if (c2 <= quad) {
-              if (weak) {
+        }
+        if (b + b_step >= 4) arrive(AGG ? &ms.empty_v[st] : &ms.v_read[st]);
+        // M4 has read the buffer's last content (two phases per chunk: the one before this is b / 2 - 1)
+        if ((n > 0 || b >= 2) && !wait(&ms.vp_free[buf], (uint32_t)((b >> 1) ^ 1))) return false;
+        if (has_ch) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                  const float4 w = *reinterpret_cast<const float4 *>(&g.G[32 * c2 + j]);
-                  const float2 a = __fmul2_rn(make_float2(x[j], x[j + 1]), make_float2(w.x, w.y));
-                  const float2 b = __fmul2_rn(make_float2(x[j + 2], x[j + 3]), make_float2(w.z, w.w));
-                  x[j] = a.x; x[j + 1] = a.y; x[j + 2] = b.x; x[j + 3] = b.y;
-                }
-              } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] *= ex2_approx(Gr - g.G[32 * c2 + j]);
-              }
-              if (c2 == quad) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
-              }
-#pragma unroll
-              for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) pk[j] = 0u;
-            }
-            umma::tmem_st16(tmem + kTmP + lane_base + c2 * 16, pk);
+          for (int hh = 0; hh < 2; ++hh) {   // 16 channels each
+            const uint32_t dst = tmem + kTmVp + buf * kTmVpBuf + lane_base + ((uint32_t)(hh * 16) << 16);
+            umma::tmem_st_16x128b_x4(dst, t0 + 8 * hh);
+            umma::tmem_st_16x128b_x4(dst + 16, t1 + 8 * hh);
+            umma::tmem_st_16x128b_x4(dst + 32, t2 + 8 * hh);
           }
           umma::tmem_st_wait();
-          arrive(&ms.p_rdy);
         }
+        arrive(&ms.vp_rdy[buf]);
       }
+      return true;
+    }, nothing);
+    if (!AGG && wg == 0) for_chunks(nothing, [&](const LaItem &, int, int, int, int n) {
+      const int st = n % kStages;
+      if (!wait(&ms.gate[st], (uint32_t)((n / kStages) & 1))) return false;
+      const LaGate &g = gates[st];
+      const bool weak = g.weak != 0;
+      const float Gr = weak ? 0.f : g.G[row] - fmaxf(g.G[row], kLaRowLog2);   // G_i - R_i
+      if (!wait(&ms.p_raw, (uint32_t)(n & 1))) return false;
+      // block c of P goes to columns 16 c .. of the scores, block c / 2 of them: read by then
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+        if (c <= quad) {
+          float x[32];
+          umma::tmem_ld32(tmem + kTmP + lane_base + c * 32, x);
+          umma::tmem_ld_wait();
+          if (weak) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 w = *reinterpret_cast<const float4 *>(&g.G[32 * c + j]);
+              const float2 a = __fmul2_rn(make_float2(x[j], x[j + 1]), make_float2(w.x, w.y));
+              const float2 b = __fmul2_rn(make_float2(x[j + 2], x[j + 3]), make_float2(w.z, w.w));
+              x[j] = a.x; x[j + 1] = a.y; x[j + 2] = b.x; x[j + 3] = b.y;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] *= ex2_approx(Gr - g.G[32 * c + j]);
+          }
+          if (c == quad) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = 0u;
+        }
+        umma::tmem_st16(tmem + kTmP + lane_base + c * 16, pk);
+      }
+      umma::tmem_st_wait();
+      arrive(&ms.p_rdy);
+      arrive(&ms.empty[st]);
       return true;
     }, nothing);
   } else if (warp < 16) {
@@ -690,14 +703,25 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
     const bool has_v = (warp & 3) * 32 < V;    // lanes are value columns of S^T, token rows of O
     float S[KH];
     float seg_decay = 1.f;
-    auto copy_s = [&](int x) {                 // bf16 copy of columns x .. x + 31 of S^T, the operand of M2
+    uint32_t sync_phase = 0;
+    auto sync_state = [&] {
+      arrive(&ms.state_sync);
+      const bool ok = wait(&ms.state_sync, sync_phase);
+      sync_phase ^= 1u;
+      return ok;
+    };
+    auto copy_s = [&] {                        // bf16 copy of S^T, the operand of M2
+      if (has_v) {
 #pragma unroll
-      for (int j = x; j < x + 32; j += 8) {
-        const int k = half * KH + j;
-        *reinterpret_cast<uint4 *>(sm + Lay::s_off + (k >> 6) * Lay::s_panel + umma::sw128_chunk(row, (k & 63) >> 3)) =
-            make_uint4(pack_bf16(S[j], S[j + 1]), pack_bf16(S[j + 2], S[j + 3]), pack_bf16(S[j + 4], S[j + 5]),
-                       pack_bf16(S[j + 6], S[j + 7]));
+        for (int j = 0; j < KH; j += 8) {
+          const int k = half * KH + j;
+          *reinterpret_cast<uint4 *>(sm + Lay::s_off + (k >> 6) * Lay::s_panel + umma::sw128_chunk(row, (k & 63) >> 3)) =
+              make_uint4(pack_bf16(S[j], S[j + 1]), pack_bf16(S[j + 2], S[j + 3]), pack_bf16(S[j + 4], S[j + 5]),
+                         pack_bf16(S[j + 6], S[j + 7]));
+        }
       }
+      umma::fence_proxy_async_smem();
+      arrive(&ms.s_rdy);
     };
     // this warp's part of the copy's buffer, for the states' way to and from memory between items
     unsigned char *patch = sm + Lay::s_off + (half * (V / 32) + (warp & 3)) * (32 * (K / 4) * 4);
@@ -718,21 +742,16 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
             }
           }
           seg_decay = 1.f;
-          if constexpr (!AGG) umma::named_bar(6, 256);   // all patches of the copy's buffer are done with
-          if (!AGG && nch > 0) {   // M2 of the item before has read its copy (s_free)
-            if (has_v) {
-#pragma unroll
-              for (int x = 0; x < KH; x += 32) copy_s(x);
-            }
-            umma::fence_proxy_async_smem();
-            arrive(&ms.s_rdy);
+          if constexpr (!AGG) {
+            if (!sync_state()) return false;   // the states have left the copy's buffer, M2 has read it (s_free)
+            if (nch > 0) copy_s();
           }
           return true;
         },
         [&](const LaItem &it, int h, int c, int nch, int n) {
           const int st = (int)(n % kStages);
           const uint32_t ph = (uint32_t)(n & 1);
-          if (!wait(&ms.full[st], (uint32_t)((n / kStages) & 1))) return false;
+          if (!wait(&ms.gate[st], (uint32_t)((n / kStages) & 1))) return false;
           const float gamma = gates[st].gamma;
           float f = 0.f;   // scale exp(R_i) of this thread's token row
           if constexpr (!AGG) {
@@ -740,10 +759,8 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
             f = p.scale * (gates[st].weak ? rcp_approx(G) : ex2_approx(fmaxf(G, kLaRowLog2)));
           }
           arrive(&ms.empty[st]);   // the factors have been read
-          auto new_state = [&] {   // S^T = gamma S^T + D^T, and its copy for the next chunk
+          auto new_state = [&] {   // S^T = gamma S^T + D^T
             if (!wait(&ms.d_rdy, ph)) return false;
-            const bool copy = !AGG && c + 1 < nch;
-            if (!AGG && !wait(&ms.s_free, ph)) return false;   // M2 has read the copy of S
             if (has_v) {
 #pragma unroll
               for (int x = 0; x < KH; x += 32) {
@@ -757,19 +774,17 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
                   S[x + j] = a.x;
                   S[x + j + 1] = a.y;
                 }
-                if (copy) copy_s(x);
               }
             } else {
               arrive(&ms.d_free);
             }
             if constexpr (AGG) seg_decay *= gamma;
-            if (copy) {
-              umma::fence_proxy_async_smem();
-              arrive(&ms.s_rdy);
-            }
+            if (AGG) return true;
+            if (!wait(&ms.s_free, ph)) return false;   // M2 has read the copy
+            if (c + 1 < nch) copy_s();
             return true;
           };
-          auto output = [&] {      // o in bf16 over the chunk's v, which M3 and the V' warps have read
+          auto output = [&] {      // o = f O in bf16, over the chunk's v, which M3 and the V' warps have read
             if (!wait(&ms.o_done, ph) || !wait(&ms.v_read[st], (uint32_t)((n / kStages) & 1))) return false;
             unsigned char *tile = sm + st * Lay::stage + Lay::v_off;
 #pragma unroll 1
