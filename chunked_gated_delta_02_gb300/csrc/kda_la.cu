@@ -60,7 +60,7 @@ constexpr int kLaThreads = 640;
 constexpr int kLaRegsOperands = 88, kLaRegsState = 128, kLaRegsIssue = 48;
 static_assert(2 * kLaRegsOperands + 2 * kLaRegsState + kLaRegsIssue <= 5 * 96, "registers at launch");
 constexpr uint32_t kLaTmemCols = 512;
-constexpr long long kLaWaitLimit = 4000000000LL;   // ~2 s of SM clocks per wait
+constexpr unsigned kLaWaitLimit = 4000000000u;   // ~2 s of SM clocks per wait
 // The smallest log2 decay of a token: 2^-126 is the smallest normal fp32 number, so that a decay of
 // zero (log decay -inf) drops the state without an inf - inf in the sums.
 constexpr float kLaMinLog2 = -126.0f;
@@ -118,17 +118,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&x);
 }
 
-__device__ __forceinline__ LaItem la_item(const LaProblem &p, long long idx) {
+__device__ __forceinline__ LaItem la_item(const LaProblem &p, int idx) {
   LaItem it;
   if (p.cu) {
     it = p.items[idx];
   } else {
-    const int s = (int)(idx / p.n_seg), g = (int)(idx % p.n_seg);
+    const int s = idx / p.n_seg, g = idx % p.n_seg;
     it.seq = s;
     it.b = s;
     it.t0 = g * p.seg_chunks * kLaChunk;
     it.len = max(0, min(p.T - it.t0, p.seg_chunks * kLaChunk));
-    it.slot = (int)idx;
+    it.slot = idx;
     it.seg = g;
     it.n_seg = p.n_seg;
   }
@@ -136,100 +136,46 @@ __device__ __forceinline__ LaItem la_item(const LaProblem &p, long long idx) {
 }
 
 // S^T rows v0 + lane of (sequence s, head h), columns [k0, k0 + N), between a warp's registers and the
-// caller's state. In the [V, K] layout a thread's values are contiguous, but the warp's are 32 rows
-// apart: they change places in `buf`, 32 rows of K / 4 columns of shared memory that the warp has to
-// itself, so that every access covers whole 128-byte (64-byte) pieces of a row.
+// caller's state in any type and layout, by way of `buf`: 32 rows of K / 4 fp32 values of shared memory
+// that the warp has to itself. From there every access covers whole 64- or 128-byte pieces of memory,
+// and only one loop, not one per register and variant, has the memory side's code.
 template <int K, int V, int N, bool STORE>
 __device__ __forceinline__ void la_state_move(const LaProblem &p, int s, int h, int v0, int k0, float (&S)[N],
-                                              unsigned char *buf) {
+                                              float *buf) {
+  constexpr int kCols = K / 4, kChunks = kCols / 4;   // 16-byte chunk c of row r lies at chunk c ^ (r % kChunks)
   const int lane = threadIdx.x & 31;
   const long long base = ((long long)s * p.H + h) * K * V;
-  const bool bf16 = p.flags & kStateBf16;
-  const float *in32 = static_cast<const float *>(p.init) + base;
-  const __nv_bfloat16 *in16 = static_cast<const __nv_bfloat16 *>(p.init) + base;
-  float *out32 = static_cast<float *>(p.final_state) + base;
-  __nv_bfloat16 *out16 = static_cast<__nv_bfloat16 *>(p.final_state) + base;
-  if (p.flags & kStateKV) {   // a warp's values of one column are contiguous
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int i = (k0 + j) * V + v0 + lane;
-      if (STORE && bf16) out16[i] = __float2bfloat16_rn(S[j]);
-      else if (STORE) out32[i] = S[j];
-      else S[j] = bf16 ? __bfloat162float(in16[i]) : in32[i];
-    }
-    return;
-  }
-  constexpr int kCols = K / 4;
-  uint4 *b4 = reinterpret_cast<uint4 *>(buf);
+  const bool bf16 = p.flags & kStateBf16, kv = p.flags & kStateKV;
+  float4 *mine = reinterpret_cast<float4 *>(buf) + lane * kChunks;
 #pragma unroll
   for (int r = 0; r < N; r += kCols) {
-    if (bf16) {
-      constexpr int kChunks = kCols / 8;   // 16-byte chunks of a row
-      uint4 *mine = b4 + lane * kChunks;
-      auto global = [&](int i) {           // row and chunk of this lane in step i of kChunks
-        const int row = i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
-        uint4 *at = b4 + row * kChunks + (c ^ (row & (kChunks - 1)));
-        const int g = (v0 + row) * K + k0 + r + c * 8;
-        if (STORE) *reinterpret_cast<uint4 *>(out16 + g) = *at;
-        else *at = *reinterpret_cast<const uint4 *>(in16 + g);
-      };
-      if (!STORE) {
+    if (STORE) {
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) global(i);
-        __syncwarp();
+      for (int j = 0; j < kChunks; ++j)
+        mine[j ^ (lane & (kChunks - 1))] = make_float4(S[r + 4 * j], S[r + 4 * j + 1], S[r + 4 * j + 2], S[r + 4 * j + 3]);
+      __syncwarp();
+    }
+    // step i: one column of 32 rows ([K, V] layout), or 32 consecutive columns of the rows
+#pragma unroll 4
+    for (int i = 0; i < kCols; ++i) {
+      const int row = kv ? lane : (i * 32 + lane) / kCols, col = kv ? i : (i * 32 + lane) % kCols;
+      float &x = buf[row * kCols + (((col >> 2) ^ (row & (kChunks - 1))) << 2) + (col & 3)];
+      const long long g = base + (kv ? (k0 + r + col) * V + v0 + row : (v0 + row) * K + k0 + r + col);
+      if (STORE) {
+        if (bf16) static_cast<__nv_bfloat16 *>(p.final_state)[g] = __float2bfloat16_rn(x);
+        else static_cast<float *>(p.final_state)[g] = x;
+      } else {
+        x = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.init)[g]) : static_cast<const float *>(p.init)[g];
       }
+    }
+    __syncwarp();
+    if (!STORE) {
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
-        uint4 &at = mine[j ^ (lane & (kChunks - 1))];
-        float *x = &S[r + 8 * j];
-        if (STORE) {
-          at = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-        } else {
-          const uint4 w = at;
-          x[0] = __uint_as_float(w.x << 16); x[1] = __uint_as_float(w.x & 0xFFFF0000u);
-          x[2] = __uint_as_float(w.y << 16); x[3] = __uint_as_float(w.y & 0xFFFF0000u);
-          x[4] = __uint_as_float(w.z << 16); x[5] = __uint_as_float(w.z & 0xFFFF0000u);
-          x[6] = __uint_as_float(w.w << 16); x[7] = __uint_as_float(w.w & 0xFFFF0000u);
-        }
+        const float4 f = mine[j ^ (lane & (kChunks - 1))];
+        S[r + 4 * j] = f.x; S[r + 4 * j + 1] = f.y; S[r + 4 * j + 2] = f.z; S[r + 4 * j + 3] = f.w;
       }
       __syncwarp();
-      if (STORE) {
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) global(i);
-        __syncwarp();
-      }
-    } else {
-      constexpr int kChunks = kCols / 4;
-      uint4 *mine = b4 + lane * kChunks;
-      auto global = [&](int i) {
-        const int row = i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
-        uint4 *at = b4 + row * kChunks + (c ^ (row & (kChunks - 1)));
-        const int g = (v0 + row) * K + k0 + r + c * 4;
-        if (STORE) *reinterpret_cast<uint4 *>(out32 + g) = *at;
-        else *at = *reinterpret_cast<const uint4 *>(in32 + g);
-      };
-      if (!STORE) {
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) global(i);
-        __syncwarp();
-      }
-#pragma unroll
-      for (int j = 0; j < kChunks; ++j) {
-        uint4 &at = mine[j ^ (lane & (kChunks - 1))];
-        float *x = &S[r + 4 * j];
-        if (STORE) {
-          at = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-        } else {
-          const uint4 w = at;
-          x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
-        }
-      }
-      __syncwarp();
-      if (STORE) {
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) global(i);
-        __syncwarp();
-      }
     }
   }
 }
@@ -259,7 +205,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
     if (tid == 0) atomicExch(p.dev_status, kDevWaitTimeout);
     return;
   }
-  const long long total = (p.cu ? (long long)*p.n_items : (long long)p.N * p.n_seg) * p.H;
+  const int total = (p.cu ? *p.n_items : p.N * p.n_seg) * p.H;   // below 2^31 (kda_la_fwd)
 
   if (warp == 0) {
     umma::tmem_alloc(&ms.tmem_slot, kLaTmemCols);
@@ -303,11 +249,11 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
   // Bounded wait of one thread; it ends early once any wait of the CTA has given up.
   auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool {
     if (umma::mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
+    const unsigned t0 = (unsigned)clock();
     while (!umma::mbar_try_wait(bar, parity)) {
       if (*(volatile int *)&ms.err) return false;
-      if (clock64() - t0 > kLaWaitLimit) {
-        atomicExch(&ms.err, 1);
+      if ((unsigned)clock() - t0 > kLaWaitLimit) {
+        *(volatile int *)&ms.err = 1;
         return false;
       }
     }
@@ -331,11 +277,12 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
     // The items come longest first: rounds of one item per CTA, every other round backwards, even out
     // what the CTAs get.
     int n = 0;
-    for (long long round = 0; round * gridDim.x < total; ++round) {
-      const long long w = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    const int ctas = gridDim.x, cta = blockIdx.x;
+    for (int first = 0, w0 = cta; first < total; first += ctas, w0 = ctas - 1 - w0) {
+      const int w = first + w0;
       if (w >= total) continue;
       const LaItem it = la_item(p, w / p.H);
-      const int h = (int)(w % p.H);
+      const int h = w % p.H;
       if (AGG && it.seg == it.n_seg - 1) continue;
       const int nch = (it.len + kLaChunk - 1) / kLaChunk;
       if (!begin(it, h, nch)) return;
@@ -724,7 +671,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
       arrive(&ms.s_rdy);
     };
     // this warp's part of the copy's buffer, for the states' way to and from memory between items
-    unsigned char *patch = sm + Lay::s_off + (half * (V / 32) + (warp & 3)) * (32 * (K / 4) * 4);
+    float *patch = reinterpret_cast<float *>(sm + Lay::s_off) + (half * (V / 32) + (warp & 3)) * (32 * (K / 4));
     auto seg_block = [&](int slot, int h) { return p.seg_state + ((long long)slot * p.H + h) * (K * V); };
     for_chunks(
         [&](const LaItem &it, int h, int nch) {
