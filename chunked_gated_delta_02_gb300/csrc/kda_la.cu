@@ -83,8 +83,9 @@ struct LaMisc {
   // per stage: q and k loaded, consumed; v loaded, consumed; decay factors written (consumed with q and
   // k); v rows past the sequence cleared; V' formed; output tile written over v
   uint64_t full[3], empty[3], full_v[3], empty_v[3], gate[3], v_rdy[3], v_read[3], o_st[3];
-  uint64_t p_raw, p_rdy, s_free, o_done, o_free, d_rdy, d_free, s_rdy;   // one phase per chunk
-  uint64_t vp_rdy[2], vp_free[2];                   // per V' buffer: 32 tokens ready, read
+  uint64_t p_raw, p_rdy, s_free, o_done, o_free, s_rdy;   // one phase per chunk
+  uint64_t vp_rdy[4], vp_free[4];                   // per V' buffer: 32 tokens ready, read
+  uint64_t d_rdy[2], d_free[2];                     // per D buffer: ready, read
   uint64_t state_sync;                              // the state warps among themselves
   uint64_t bar_exit;
   uint32_t tmem_slot;
@@ -112,6 +113,8 @@ constexpr uint32_t kTmVp = 128;   // V'^T: two buffers of 32 tokens, three terms
 constexpr uint32_t kTmVpBuf = 48;
 constexpr uint32_t kTmO = 256;    // O, V columns
 constexpr uint32_t kTmD = 384;    // D^T, K columns
+// Without scores and O, V' has a buffer for every 32 tokens of a chunk, and D^T two.
+constexpr uint32_t kTmVpAgg = 0, kTmDAgg = 256;
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
@@ -205,7 +208,8 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
     if (tid == 0) atomicExch(p.dev_status, kDevWaitTimeout);
     return;
   }
-  const int total = (p.cu ? *p.n_items : p.N * p.n_seg) * p.H;   // below 2^31 (kda_la_fwd)
+  const int total = (p.cu ? p.counts[AGG ? 1 : 0] : p.N * p.n_seg) * p.H;   // below 2^31 (kda_la_fwd)
+  if (total == 0) return;
 
   if (warp == 0) {
     umma::tmem_alloc(&ms.tmem_slot, kLaTmemCols);
@@ -222,9 +226,13 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
       umma::mbar_init(&ms.v_read[s], 4);
       umma::mbar_init(&ms.o_st[s], 8);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 4; ++b) {
       umma::mbar_init(&ms.vp_rdy[b], 4);
       umma::mbar_init(&ms.vp_free[b], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      umma::mbar_init(&ms.d_rdy[b], 1);
+      umma::mbar_init(&ms.d_free[b], 8);
     }
     umma::mbar_init(&ms.p_raw, 1);
     umma::mbar_init(&ms.p_rdy, 4);
@@ -232,8 +240,6 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
     umma::mbar_init(&ms.o_done, 1);
     umma::mbar_init(&ms.o_free, 8);
     umma::mbar_init(&ms.state_sync, 8);
-    umma::mbar_init(&ms.d_rdy, 1);
-    umma::mbar_init(&ms.d_free, 8);
     umma::mbar_init(&ms.s_rdy, 8);
     umma::mbar_init(&ms.bar_exit, 2);
     umma::mbar_fence_init();
@@ -250,14 +256,16 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
   auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool {
     if (umma::mbar_try_wait(bar, parity)) return true;
     const unsigned t0 = (unsigned)clock();
-    while (!umma::mbar_try_wait(bar, parity)) {
+    while (true) {
+#pragma unroll 1
+      for (int i = 0; i < 64; ++i)
+        if (umma::mbar_try_wait(bar, parity)) return true;
       if (*(volatile int *)&ms.err) return false;
       if ((unsigned)clock() - t0 > kLaWaitLimit) {
         *(volatile int *)&ms.err = 1;
         return false;
       }
     }
-    return true;
   };
   // The same for a whole warp, with one answer.
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -421,30 +429,35 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
         if (!wait(&ms.full[st], sph)) return false;
         // M1: scores = Q K^T (the scores of the chunk before were last read by its M3, ahead of this in order)
         if (umma::elect_one()) {
+#pragma unroll 1
+          for (int x = 0; x < K / 64; ++x)
 #pragma unroll
-          for (int x = 0; x < K / 16; ++x) {
-            const uint32_t off = (x / 4) * Lay::panel + (x % 4) * 32;
-            umma::mma_f16_ss(tmem + kTmP, umma::desc_add(aq, off), umma::desc_add(bk, off), id1, x > 0);
-          }
+            for (int y = 0; y < 4; ++y)
+              umma::mma_f16_ss(tmem + kTmP, umma::desc_add(aq, x * Lay::panel + y * 32),
+                               umma::desc_add(bk, x * Lay::panel + y * 32), id1, x + y > 0);
           umma::commit(&ms.p_raw);
         }
         // M2: O = Q S
         if (!wait(&ms.s_rdy, ph)) return false;
         if (n > 0 && !wait(&ms.o_free, ph ^ 1u)) return false;
         if (umma::elect_one()) {
+#pragma unroll 1
+          for (int x = 0; x < K / 64; ++x)
 #pragma unroll
-          for (int x = 0; x < K / 16; ++x)
-            umma::mma_f16_ss(tmem + kTmO, umma::desc_add(aq, (x / 4) * Lay::panel + (x % 4) * 32),
-                             umma::desc_add(bs, (x / 4) * Lay::s_panel + (x % 4) * 32), id2, x > 0);
+            for (int y = 0; y < 4; ++y)
+              umma::mma_f16_ss(tmem + kTmO, umma::desc_add(aq, x * Lay::panel + y * 32),
+                               umma::desc_add(bs, x * Lay::s_panel + y * 32), id2, x + y > 0);
           umma::commit(&ms.s_free);
           umma::commit(&ms.empty[st]);
         }
         // M3: O += P V; v_rdy: rows of the v tile past the sequence have been cleared
         if (!wait(&ms.v_rdy[st], sph) || !wait(&ms.p_rdy, ph)) return false;
         if (umma::elect_one()) {
+#pragma unroll 1
+          for (int x = 0; x < 8; x += 4)
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            umma::mma_f16_ts(tmem + kTmO, tmem + kTmP + x * 8, umma::desc_add(bv, x * 2048), id3, 1);
+            for (int y = 0; y < 4; ++y)
+              umma::mma_f16_ts(tmem + kTmO, tmem + kTmP + (x + y) * 8, umma::desc_add(bv, (x + y) * 2048), id3, 1);
           umma::commit(&ms.o_done);
         }
         __syncwarp();
@@ -459,19 +472,21 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
       const int st = n % kStages;
       const uint64_t kt = umma::sdesc_sw128(sbase + st * Lay::stage + Lay::k_off, Lay::panel, 1024);
       if (!wait(&ms.full[st], (uint32_t)((n / kStages) & 1))) return false;
-      if (n > 0 && !wait(&ms.d_free, (uint32_t)((n - 1) & 1))) return false;
-#pragma unroll
+      const int di = AGG ? n & 1 : 0;
+      const uint32_t dph = (uint32_t)((AGG ? n >> 1 : n) & 1), tD = tmem + (AGG ? kTmDAgg + di * 128 : kTmD);
+      if (n >= (AGG ? 2 : 1) && !wait(&ms.d_free[di], dph ^ 1u)) return false;
+#pragma unroll 1
       for (int b = 0; b < 4; ++b) {   // 32 tokens: two steps of 16, three terms
-        const int buf = b & 1;
-        if (!wait(&ms.vp_rdy[buf], (uint32_t)(b >> 1))) return false;   // two phases per chunk: 0 and 1
+        const int buf = AGG ? b : b & 1;   // of two buffers, each has two phases per chunk
+        if (!wait(&ms.vp_rdy[buf], (uint32_t)(AGG ? n & 1 : b >> 1))) return false;
         if (umma::elect_one()) {
 #pragma unroll
           for (int x = 0; x < 6; ++x)
-            umma::mma_f16_ts(tmem + kTmD, tmem + kTmVp + buf * kTmVpBuf + x * 8,
+            umma::mma_f16_ts(tD, tmem + (AGG ? kTmVpAgg : kTmVp) + buf * kTmVpBuf + x * 8,
                              umma::desc_add(kt, (2 * b + (x & 1)) * 2048), id4, b > 0 || x > 0);
           umma::commit(&ms.vp_free[buf]);
           if (b == 3) {
-            umma::commit(&ms.d_rdy);
+            umma::commit(&ms.d_rdy[di]);
             umma::commit(&ms.empty[st]);
           }
         }
@@ -518,7 +533,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
     // 16 channels x 16 tokens; lane l names token l % 8 of matrix l / 8
     const int ch0 = quad * 32 + ((lane >> 3) & 1) * 8;
     const uint32_t v_src = (uint32_t)((ch0 >> 6) * Lay::panel + ((lane >> 4) * 8 + (lane & 7)) * 128);
-    // Without P to form, both warpgroups take every other 32 tokens of V', with a buffer of their own.
+    // Without P to form, both warpgroups take every other 32 tokens of V'.
     const int b_first = AGG ? wg : 0, b_step = AGG ? 2 : 1;
     // The roles' loops stay rolled: each warp runs alone on its scheduler in its role, and code that does
     // not repeat is fetched at every step (fully unrolled, P and V' took twice as long).
@@ -546,54 +561,54 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
       const LaGate &g = gates[st];
 #pragma unroll 1
       for (int b = b_first; b < 4; b += b_step) {
-        const int buf = b & 1;
-        uint32_t t0[16], t1[16], t2[16];   // the three terms, [16 channels][8-token block][8 channels]
-        if (has_ch) {
-          uint32_t raw[16];
-          const uint32_t src = umma::smem_u32(vt) + v_src + (uint32_t)(32 * b * 128);
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              umma::ldmatrix_x4_trans(src + 16 * i * 128 + (uint32_t)(((((ch0 & 63) >> 3) + 2 * hh) ^ (lane & 7)) << 4),
-                                      raw[8 * hh + 4 * i], raw[8 * hh + 4 * i + 1], raw[8 * hh + 4 * i + 2], raw[8 * hh + 4 * i + 3]);
-          if (L < kLaChunk) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {   // tokens t and t + 1 of a pair
-              const int t = 32 * b + 8 * ((r >> 1) & 3) + 2 * (lane & 3);
-              raw[r] &= t + 1 < L ? 0xFFFFFFFFu : t < L ? 0xFFFFu : 0u;
-            }
-          }
+        const int buf = AGG ? b : b & 1;
+        // M4 has read the buffer's last content, of the chunk before or of block b - 2
+        auto buffer_free = [&] {
+          return AGG ? n == 0 || wait(&ms.vp_free[buf], (uint32_t)((n - 1) & 1))
+                     : (n == 0 && b < 2) || wait(&ms.vp_free[buf], (uint32_t)((b >> 1) ^ 1));
+        };
+        if (!has_ch) {
+          if (!buffer_free()) return false;
+        } else {
           const float bf = g.bf[b];
           const float2 minus = make_float2(-1.f, -1.f);
+          float2 w[4];   // factors of tokens 8 m + 2 (l % 4) and the next
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {   // factors of tokens 8 m + 2 (l % 4) and the next
-            const float2 w = __fmul2_rn(*reinterpret_cast<const float2 *>(&g.cf[32 * b + 8 * m + 2 * (lane & 3)]), make_float2(bf, bf));
+          for (int m = 0; m < 4; ++m)
+            w[m] = __fmul2_rn(*reinterpret_cast<const float2 *>(&g.cf[32 * b + 8 * m + 2 * (lane & 3)]), make_float2(bf, bf));
+#pragma unroll (AGG ? 2 : 1)
+          for (int hh = 0; hh < 2; ++hh) {   // 16 channels each
+            uint32_t raw[8], t0[8], t1[8], t2[8];   // [8-token block][8 channels]; the three terms
+            const uint32_t src = umma::smem_u32(vt) + v_src + (uint32_t)(32 * b * 128) +
+                                 (uint32_t)(((((ch0 & 63) >> 3) + 2 * hh) ^ (lane & 7)) << 4);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {   // token pairs of channels 16 (e / 2) + 8 (e % 2)
-              const int r = 8 * (e >> 1) + 2 * m + (e & 1);
-              float2 x = __fmul2_rn(make_float2(__uint_as_float(raw[r] << 16), __uint_as_float(raw[r] & 0xFFFF0000u)), w);
+            for (int i = 0; i < 2; ++i)
+              umma::ldmatrix_x4_trans(src + 16 * i * 128, raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
+            if (L < kLaChunk) {
+#pragma unroll
+              for (int r = 0; r < 8; ++r) {   // tokens t and t + 1 of a pair
+                const int t = 32 * b + 8 * (r >> 1) + 2 * (lane & 3);
+                raw[r] &= t + 1 < L ? 0xFFFFFFFFu : t < L ? 0xFFFFu : 0u;
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {   // token pairs of channels 8 (r % 2)
+              float2 x = __fmul2_rn(make_float2(__uint_as_float(raw[r] << 16), __uint_as_float(raw[r] & 0xFFFF0000u)), w[r >> 1]);
               t0[r] = pack_bf16(x.x, x.y);
               x = __ffma2_rn(make_float2(__uint_as_float(t0[r] << 16), __uint_as_float(t0[r] & 0xFFFF0000u)), minus, x);
               t1[r] = pack_bf16(x.x, x.y);
               x = __ffma2_rn(make_float2(__uint_as_float(t1[r] << 16), __uint_as_float(t1[r] & 0xFFFF0000u)), minus, x);
               t2[r] = pack_bf16(x.x, x.y);
             }
-          }
-        }
-        if (b + b_step >= 4) arrive(AGG ? &ms.empty_v[st] : &ms.v_read[st]);
-        // M4 has read the buffer's last content (two phases per chunk: the one before this is b / 2 - 1)
-        if ((n > 0 || b >= 2) && !wait(&ms.vp_free[buf], (uint32_t)((b >> 1) ^ 1))) return false;
-        if (has_ch) {
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {   // 16 channels each
-            const uint32_t dst = tmem + kTmVp + buf * kTmVpBuf + lane_base + ((uint32_t)(hh * 16) << 16);
-            umma::tmem_st_16x128b_x4(dst, t0 + 8 * hh);
-            umma::tmem_st_16x128b_x4(dst + 16, t1 + 8 * hh);
-            umma::tmem_st_16x128b_x4(dst + 32, t2 + 8 * hh);
+            if (hh == 0 && !buffer_free()) return false;
+            const uint32_t dst = tmem + (AGG ? kTmVpAgg : kTmVp) + buf * kTmVpBuf + lane_base + ((uint32_t)(hh * 16) << 16);
+            umma::tmem_st_16x128b_x4(dst, t0);
+            umma::tmem_st_16x128b_x4(dst + 16, t1);
+            umma::tmem_st_16x128b_x4(dst + 32, t2);
           }
           umma::tmem_st_wait();
         }
+        if (b + b_step >= 4) arrive(AGG ? &ms.empty_v[st] : &ms.v_read[st]);
         arrive(&ms.vp_rdy[buf]);
       }
       return true;
@@ -707,14 +722,15 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           }
           arrive(&ms.empty[st]);   // the factors have been read
           auto new_state = [&] {   // S^T = gamma S^T + D^T
-            if (!wait(&ms.d_rdy, ph)) return false;
+            const int di = AGG ? n & 1 : 0;
+            if (!wait(&ms.d_rdy[di], (uint32_t)((AGG ? n >> 1 : n) & 1))) return false;
             if (has_v) {
 #pragma unroll
               for (int x = 0; x < KH; x += 32) {
                 float y[32];
-                umma::tmem_ld32(tmem + kTmD + lane_base + half * KH + x, y);
+                umma::tmem_ld32(tmem + (AGG ? kTmDAgg + di * 128 : kTmD) + lane_base + half * KH + x, y);
                 umma::tmem_ld_wait();
-                if (x + 32 >= KH) arrive(&ms.d_free);
+                if (x + 32 >= KH) arrive(&ms.d_free[di]);
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
                   const float2 a = __ffma2_rn(make_float2(gamma, gamma), make_float2(S[x + j], S[x + j + 1]), make_float2(y[j], y[j + 1]));
@@ -723,7 +739,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
                 }
               }
             } else {
-              arrive(&ms.d_free);
+              arrive(&ms.d_free[di]);
             }
             if constexpr (AGG) seg_decay *= gamma;
             if (AGG) return true;
@@ -759,7 +775,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           };
           if constexpr (AGG) return new_state();
           // whichever product is done first; rolled, so that each part is one piece of code
-          const bool state_first = __all_sync(0xffffffffu, umma::mbar_test(&ms.d_rdy, ph));
+          const bool state_first = __all_sync(0xffffffffu, umma::mbar_test(&ms.d_rdy[0], ph));
 #pragma unroll 1
           for (int part = 0; part < 2; ++part)
             if (!((part == 0) == state_first ? new_state() : output())) return false;
@@ -796,12 +812,16 @@ template <int K, int V>
 __global__ void __launch_bounds__(256) la_combine_kernel(const LaProblem p) {
   pdl_wait();
   if (p.flag && *p.flag != kDevOk) return;
-  const int s = blockIdx.x / p.H, h = blockIdx.x % p.H;
+  const int h = blockIdx.x % p.H;
+  int s = blockIdx.x / p.H;
+  if (p.cu) {
+    if (s >= p.counts[2]) return;
+    s = p.multi[s];
+  }
   const int slot0 = p.cu ? p.slot0[s] : s * p.n_seg;
   const int n = p.cu ? p.slot0[s + 1] - slot0 : p.n_seg;
   const int x = blockIdx.y * 256 + threadIdx.x;             // float4 index of the block
   const int j = x / (2 * V), half = (x / V) & 1, v = x % V;
-  if (n < 2) return;
   float S[4] = {0.f, 0.f, 0.f, 0.f};
   if (p.init) {
     const long long base = ((long long)s * p.H + h) * (K * V);
@@ -840,24 +860,48 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const LaProblem p) {
 }
 
 // Varlen schedule: checks cu_seqlens, cuts the sequences into segments of seg_chunks chunks and lists
-// them longest first (counting sort; very long segments share bins, which only makes the order
-// approximate). One CTA.
+// them: first the segments whose states are formed ahead (all but the last of a sequence, equally
+// long), then the others, longest first (counting sort; very long ones share bins, which only makes
+// the order approximate). Also lists the sequences of more than one segment. One CTA.
 constexpr int kLaSchedThreads = 1024, kLaSchedBins = 2048;
 
+// Exclusive sum over the CTA's threads, and the total; `part` holds 33 ints.
+__device__ __forceinline__ int block_exclusive_sum(int x, int *part, int &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = x;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, m);
+    if (lane >= m) incl += y;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    int t = part[lane], ti = t;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, ti, m);
+      if (lane >= m) ti += y;
+    }
+    part[lane] = ti - t;
+    if (lane == 31) part[32] = ti;
+  }
+  __syncthreads();
+  total = part[32];
+  return part[warp] + incl - x;
+}
+
 __global__ void __launch_bounds__(kLaSchedThreads) la_schedule_kernel(const LaProblem p) {
-  __shared__ int s_bad;
-  __shared__ int s_scan[kLaSchedThreads];
+  __shared__ int s_part[33];
   __shared__ int s_bins[kLaSchedBins];
   pdl_launch_dependents();
   const int tid = threadIdx.x, N = p.N;
   const int32_t *cu = p.cu;
-  if (tid == 0) s_bad = (cu[0] != 0 || cu[N] != p.T) ? 1 : 0;
+  bool bad = tid == 0 && (cu[0] != 0 || cu[N] != p.T);
+  for (int i = tid; i < N; i += kLaSchedThreads) bad |= cu[i + 1] < cu[i];
   for (int b = tid; b < kLaSchedBins; b += kLaSchedThreads) s_bins[b] = 0;
-  __syncthreads();
-  for (int i = tid; i < N; i += kLaSchedThreads)
-    if (cu[i + 1] < cu[i]) atomicOr(&s_bad, 1);
-  __syncthreads();
-  if (s_bad) {
+  if (__syncthreads_or(bad)) {
     if (tid == 0) {
       *p.flag = kDevBadCuSeqlens;
       atomicExch(p.dev_status, kDevBadCuSeqlens);
@@ -868,61 +912,55 @@ __global__ void __launch_bounds__(kLaSchedThreads) la_schedule_kernel(const LaPr
   const int longest = min(p.seg_chunks, (p.T + kLaChunk - 1) / kLaChunk);
   const int per_bin = longest / kLaSchedBins + 1;   // chunk counts per bin; bins in descending order
   auto bin_of = [&](int chunks) { return (longest - chunks) / per_bin; };
-  int carry = 0;
+  // slots of the sequences' segments; how many segments are formed ahead, how many sequences have any
+  int slots = 0, ahead = 0, multi = 0;
   for (int base = 0; base < N; base += kLaSchedThreads) {
     const int i = base + tid;
     int n = 0;
     if (i < N) {
       const int nc = (cu[i + 1] - cu[i] + kLaChunk - 1) / kLaChunk;
       n = max(1, (nc + p.seg_chunks - 1) / p.seg_chunks);
-      if (n > 1) atomicAdd(&s_bins[0], n - 1);
       atomicAdd(&s_bins[bin_of(nc - (n - 1) * p.seg_chunks)], 1);
     }
-    s_scan[tid] = n;
-    __syncthreads();
-    for (int off = 1; off < kLaSchedThreads; off <<= 1) {
-      const int x = (tid >= off) ? s_scan[tid - off] : 0;
-      __syncthreads();
-      s_scan[tid] += x;
-      __syncthreads();
-    }
-    if (i < N) p.slot0[i] = carry + s_scan[tid] - n;
-    carry += s_scan[kLaSchedThreads - 1];
-    __syncthreads();
+    int total, many;
+    const int before = block_exclusive_sum(n, s_part, total);
+    const int rank = block_exclusive_sum(n > 1, s_part, many);
+    if (i < N) p.slot0[i] = slots + before;
+    if (n > 1) p.multi[multi + rank] = i;
+    ahead += total - min(N - base, kLaSchedThreads);
+    slots += total;
+    multi += many;
   }
   if (tid == 0) {
-    p.slot0[N] = carry;
-    *p.n_items = carry;
+    p.slot0[N] = slots;
+    p.counts[0] = slots;
+    p.counts[1] = ahead;
+    p.counts[2] = multi;
   }
-  // exclusive scan of the bins, two per thread
+  // start positions of the bins, two per thread, after the segments formed ahead
+  __syncthreads();
   const int x0 = s_bins[2 * tid], x1 = s_bins[2 * tid + 1];
-  s_scan[tid] = x0 + x1;
+  int total;
+  const int at = ahead + block_exclusive_sum(x0 + x1, s_part, total);
+  s_bins[2 * tid] = at;
+  s_bins[2 * tid + 1] = at + x0;
   __syncthreads();
-  for (int off = 1; off < kLaSchedThreads; off <<= 1) {
-    const int x = (tid >= off) ? s_scan[tid - off] : 0;
-    __syncthreads();
-    s_scan[tid] += x;
-    __syncthreads();
-  }
-  s_bins[2 * tid] = s_scan[tid] - x0 - x1;
-  s_bins[2 * tid + 1] = s_scan[tid] - x1;
-  __syncthreads();
+  const int seg_len = p.seg_chunks * kLaChunk;
   for (int i = tid; i < N; i += kLaSchedThreads) {
-    const int t0 = cu[i], len = cu[i + 1] - t0;
+    const int t0 = cu[i], len = cu[i + 1] - t0, slot0 = p.slot0[i];
     const int nc = (len + kLaChunk - 1) / kLaChunk, n = max(1, (nc + p.seg_chunks - 1) / p.seg_chunks);
-    const int seg_len = p.seg_chunks * kLaChunk;
-    const int first = n > 1 ? atomicAdd(&s_bins[0], n - 1) : 0;
     for (int g = 0; g < n; ++g) {
       LaItem it;
       it.seq = i;
       it.b = 0;
       it.seg = g;
       it.n_seg = n;
-      it.slot = p.slot0[i] + g;
-      it.t0 = n > 1 ? t0 + g * seg_len : t0;
+      it.slot = slot0 + g;
+      it.t0 = g ? t0 + g * seg_len : t0;
       it.len = g < n - 1 ? seg_len : len - (it.t0 - t0);
       it.pad = 0;
-      const int pos = g < n - 1 ? first + g : atomicAdd(&s_bins[bin_of(nc - (n - 1) * p.seg_chunks)], 1);
+      // (a sequence's segments before its last have slot0 - i segments formed ahead before them)
+      const int pos = g < n - 1 ? slot0 - i + g : atomicAdd(&s_bins[bin_of(nc - (n - 1) * p.seg_chunks)], 1);
       p.items[pos] = it;
     }
   }
@@ -935,7 +973,8 @@ __global__ void __launch_bounds__(kLaSchedThreads) la_schedule_kernel(const LaPr
 struct LaPlan {
   int seg_chunks, n_seg;
   long long slots;
-  bool segments;   // whether any sequence may have more than one segment
+  bool segments;       // whether any sequence may have more than one segment
+  long long multi;     // how many may
 };
 
 // Time model of a call, in microseconds: `rounds` of items of `chunks` chunks each per CTA, in the
@@ -978,6 +1017,7 @@ static LaPlan la_plan(int T, int H, int K, int V, int N, bool varlen) {
     r.n_seg = (nc + r.seg_chunks - 1) / r.seg_chunks;
     r.segments = r.n_seg > 1;
     r.slots = (long long)N * r.n_seg;
+    r.multi = N;
     return r;
   }
   // The lengths are on the device: segments as for equal lengths, and never longer than what an SM has
@@ -987,13 +1027,14 @@ static LaPlan la_plan(int T, int H, int K, int V, int N, bool varlen) {
   r.seg_chunks = la_segment_chunks((long long)N * H, nc_mean, K, V, sms);
   if (r.seg_chunks >= nc_mean) r.seg_chunks = std::max(nc_mean, std::max(share, 8));
   r.n_seg = 1;
-  r.segments = r.seg_chunks < nc;
+  r.multi = std::min((long long)N, (long long)T / ((long long)r.seg_chunks * kLaChunk));
+  r.segments = r.multi > 0;
   r.slots = (long long)T / ((long long)r.seg_chunks * kLaChunk) + 2ll * N;
   return r;
 }
 
 struct LaScratch {
-  size_t flag, n_items, slot0, items, decay, state, total;
+  size_t flag, counts, slot0, multi, items, decay, state, total;
 };
 static LaScratch la_scratch(const LaPlan &pl, int H, int K, int V, int N, bool varlen) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -1001,10 +1042,12 @@ static LaScratch la_scratch(const LaPlan &pl, int H, int K, int V, int N, bool v
   size_t off = 0;
   if (varlen) {
     s.flag = off;
-    s.n_items = off + 4;
-    off = up(off + 8);
+    s.counts = off + 4;
+    off = up(off + 16);
     s.slot0 = off;
     off = up(off + 4 * ((size_t)N + 1));
+    s.multi = off;
+    off = up(off + 4 * (size_t)pl.multi);
     s.items = off;
     off = up(off + sizeof(LaItem) * (size_t)pl.slots);
   }
@@ -1042,7 +1085,7 @@ static cudaError_t launch_la(const LaProblem &p, const LaMaps &maps, const LaPla
   if (pl.segments) {
     cudaError_t e = launch_la_t<K, V, true>(p, maps, items, s, overlap);
     if (e == cudaSuccess)
-      e = launch_kernel(la_combine_kernel<K, V>, dim3((unsigned)(p.N * p.H), K * V / 1024), dim3(256), 0, s, true, p);
+      e = launch_kernel(la_combine_kernel<K, V>, dim3((unsigned)(pl.multi * p.H), K * V / 1024), dim3(256), 0, s, true, p);
     if (e != cudaSuccess) return e;
     overlap = true;
   }
@@ -1116,7 +1159,8 @@ kda_status_t kda_la_fwd(const void *q, const void *k, const void *v, const float
   p.o = static_cast<__nv_bfloat16 *>(o);
   if (varlen) {
     p.flag = reinterpret_cast<int32_t *>(base + L.flag);
-    p.n_items = reinterpret_cast<int32_t *>(base + L.n_items);
+    p.counts = reinterpret_cast<int32_t *>(base + L.counts);
+    p.multi = reinterpret_cast<int32_t *>(base + L.multi);
     p.slot0 = reinterpret_cast<int32_t *>(base + L.slot0);
     p.items = reinterpret_cast<LaItem *>(base + L.items);
   }

@@ -29,9 +29,13 @@ struct LaProblem {
   // seg_decay[s H + h] is the product of its decays.
   float *seg_state;
   float *seg_decay;
-  LaItem *items;                 // varlen work list, longest first (schedule kernel)
-  int32_t *n_items;
-  int32_t *slot0;                // [N] first slot of each sequence (varlen)
+  // Varlen, by the schedule kernel: the work list, the segments formed ahead first; how many items, how
+  // many of them are formed ahead, and how many sequences have such; the first slot of each sequence
+  // [N + 1]; the sequences of more than one segment.
+  LaItem *items;
+  int32_t *counts;
+  int32_t *slot0;
+  int32_t *multi;
   int32_t *flag;                 // per-call data-error flag (varlen) or null
   int *dev_status;
   float scale;
