@@ -256,16 +256,14 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
   auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool {
     if (umma::mbar_try_wait(bar, parity)) return true;
     const unsigned t0 = (unsigned)clock();
-    while (true) {
-#pragma unroll 1
-      for (int i = 0; i < 64; ++i)
-        if (umma::mbar_try_wait(bar, parity)) return true;
+    while (!umma::mbar_try_wait(bar, parity)) {
       if (*(volatile int *)&ms.err) return false;
       if ((unsigned)clock() - t0 > kLaWaitLimit) {
         *(volatile int *)&ms.err = 1;
         return false;
       }
     }
+    return true;
   };
   // The same for a whole warp, with one answer.
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -475,7 +473,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
       const int di = AGG ? n & 1 : 0;
       const uint32_t dph = (uint32_t)((AGG ? n >> 1 : n) & 1), tD = tmem + (AGG ? kTmDAgg + di * 128 : kTmD);
       if (n >= (AGG ? 2 : 1) && !wait(&ms.d_free[di], dph ^ 1u)) return false;
-#pragma unroll 1
+#pragma unroll (AGG ? 4 : 1)
       for (int b = 0; b < 4; ++b) {   // 32 tokens: two steps of 16, three terms
         const int buf = AGG ? b : b & 1;   // of two buffers, each has two phases per chunk
         if (!wait(&ms.vp_rdy[buf], (uint32_t)(AGG ? n & 1 : b >> 1))) return false;
@@ -567,44 +565,48 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           return AGG ? n == 0 || wait(&ms.vp_free[buf], (uint32_t)((n - 1) & 1))
                      : (n == 0 && b < 2) || wait(&ms.vp_free[buf], (uint32_t)((b >> 1) ^ 1));
         };
-        if (!has_ch) {
-          if (!buffer_free()) return false;
-        } else {
-          const float bf = g.bf[b];
-          const float2 minus = make_float2(-1.f, -1.f);
-          float2 w[4];   // factors of tokens 8 m + 2 (l % 4) and the next
+        uint32_t t0[16], t1[16], t2[16];
+        if (has_ch) {
+          uint32_t raw[16];
+          const uint32_t src = umma::smem_u32(vt) + v_src + (uint32_t)(32 * b * 128);
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
-            w[m] = __fmul2_rn(*reinterpret_cast<const float2 *>(&g.cf[32 * b + 8 * m + 2 * (lane & 3)]), make_float2(bf, bf));
-#pragma unroll (AGG ? 2 : 1)
-          for (int hh = 0; hh < 2; ++hh) {   // 16 channels each
-            uint32_t raw[8], t0[8], t1[8], t2[8];   // [8-token block][8 channels]; the three terms
-            const uint32_t src = umma::smem_u32(vt) + v_src + (uint32_t)(32 * b * 128) +
-                                 (uint32_t)(((((ch0 & 63) >> 3) + 2 * hh) ^ (lane & 7)) << 4);
+          for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              umma::ldmatrix_x4_trans(src + 16 * i * 128, raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
-            if (L < kLaChunk) {
+              umma::ldmatrix_x4_trans(src + 16 * i * 128 + (uint32_t)(((((ch0 & 63) >> 3) + 2 * hh) ^ (lane & 7)) << 4),
+                                      raw[8 * hh + 4 * i], raw[8 * hh + 4 * i + 1], raw[8 * hh + 4 * i + 2], raw[8 * hh + 4 * i + 3]);
+          if (L < kLaChunk) {
 #pragma unroll
-              for (int r = 0; r < 8; ++r) {   // tokens t and t + 1 of a pair
-                const int t = 32 * b + 8 * (r >> 1) + 2 * (lane & 3);
-                raw[r] &= t + 1 < L ? 0xFFFFFFFFu : t < L ? 0xFFFFu : 0u;
-              }
+            for (int r = 0; r < 16; ++r) {
+              const int t = 32 * b + 8 * ((r >> 1) & 3) + 2 * (lane & 3);
+              raw[r] &= t + 1 < L ? 0xFFFFFFFFu : t < L ? 0xFFFFu : 0u;
             }
+          }
+          const float bf = g.bf[b];
+          const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {   // token pairs of channels 8 (r % 2)
-              float2 x = __fmul2_rn(make_float2(__uint_as_float(raw[r] << 16), __uint_as_float(raw[r] & 0xFFFF0000u)), w[r >> 1]);
+          for (int m = 0; m < 4; ++m) {
+            const float2 w = __fmul2_rn(*reinterpret_cast<const float2 *>(&g.cf[32 * b + 8 * m + 2 * (lane & 3)]), make_float2(bf, bf));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = 8 * (e >> 1) + 2 * m + (e & 1);
+              float2 x = __fmul2_rn(make_float2(__uint_as_float(raw[r] << 16), __uint_as_float(raw[r] & 0xFFFF0000u)), w);
               t0[r] = pack_bf16(x.x, x.y);
               x = __ffma2_rn(make_float2(__uint_as_float(t0[r] << 16), __uint_as_float(t0[r] & 0xFFFF0000u)), minus, x);
               t1[r] = pack_bf16(x.x, x.y);
               x = __ffma2_rn(make_float2(__uint_as_float(t1[r] << 16), __uint_as_float(t1[r] & 0xFFFF0000u)), minus, x);
               t2[r] = pack_bf16(x.x, x.y);
             }
-            if (hh == 0 && !buffer_free()) return false;
+          }
+        }
+        if (!buffer_free()) return false;
+        if (has_ch) {
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
             const uint32_t dst = tmem + (AGG ? kTmVpAgg : kTmVp) + buf * kTmVpBuf + lane_base + ((uint32_t)(hh * 16) << 16);
-            umma::tmem_st_16x128b_x4(dst, t0);
-            umma::tmem_st_16x128b_x4(dst + 16, t1);
-            umma::tmem_st_16x128b_x4(dst + 32, t2);
+            umma::tmem_st_16x128b_x4(dst, t0 + 8 * hh);
+            umma::tmem_st_16x128b_x4(dst + 16, t1 + 8 * hh);
+            umma::tmem_st_16x128b_x4(dst + 32, t2 + 8 * hh);
           }
           umma::tmem_st_wait();
         }
