@@ -158,17 +158,35 @@ __device__ __forceinline__ void la_state_move(const LaProblem &p, int s, int h, 
         mine[j ^ (lane & (kChunks - 1))] = make_float4(S[r + 4 * j], S[r + 4 * j + 1], S[r + 4 * j + 2], S[r + 4 * j + 3]);
       __syncwarp();
     }
-    // step i: one column of 32 rows ([K, V] layout), or 32 consecutive columns of the rows
-#pragma unroll 4
-    for (int i = 0; i < kCols; ++i) {
-      const int row = kv ? lane : (i * 32 + lane) / kCols, col = kv ? i : (i * 32 + lane) % kCols;
-      float &x = buf[row * kCols + (((col >> 2) ^ (row & (kChunks - 1))) << 2) + (col & 3)];
+    // Step i moves four consecutive values per lane: columns of a row, or rows of a column ([K, V] layout).
+#pragma unroll (STORE ? 2 : 8)
+    for (int i = 0; i < kChunks; ++i) {
+      const int row = kv ? 4 * (lane & 7) : (i * 32 + lane) / kChunks;
+      const int col = kv ? 4 * i + (lane >> 3) : 4 * (lane % kChunks);
+      const int at = row * kCols + (((col >> 2) ^ (row & (kChunks - 1))) << 2) + (col & 3);
+      // the places of four rows of one column
+      const int at1 = (row + 1) * kCols + (((col >> 2) ^ ((row + 1) & (kChunks - 1))) << 2) + (col & 3);
+      const int at2 = (row + 2) * kCols + (((col >> 2) ^ ((row + 2) & (kChunks - 1))) << 2) + (col & 3);
+      const int at3 = (row + 3) * kCols + (((col >> 2) ^ ((row + 3) & (kChunks - 1))) << 2) + (col & 3);
       const long long g = base + (kv ? (k0 + r + col) * V + v0 + row : (v0 + row) * K + k0 + r + col);
       if (STORE) {
-        if (bf16) static_cast<__nv_bfloat16 *>(p.final_state)[g] = __float2bfloat16_rn(x);
-        else static_cast<float *>(p.final_state)[g] = x;
+        const float4 f = kv ? make_float4(buf[at], buf[at1], buf[at2], buf[at3]) : *reinterpret_cast<const float4 *>(buf + at);
+        if (bf16) *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.final_state) + g) = make_uint2(pack_bf16(f.x, f.y), pack_bf16(f.z, f.w));
+        else *reinterpret_cast<float4 *>(static_cast<float *>(p.final_state) + g) = f;
       } else {
-        x = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.init)[g]) : static_cast<const float *>(p.init)[g];
+        float4 f;
+        if (bf16) {
+          const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.init) + g);
+          f = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                          __uint_as_float(u.y & 0xFFFF0000u));
+        } else {
+          f = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.init) + g);
+        }
+        if (kv) {
+          buf[at] = f.x; buf[at1] = f.y; buf[at2] = f.z; buf[at3] = f.w;
+        } else {
+          *reinterpret_cast<float4 *>(buf + at) = f;
+        }
       }
     }
     __syncwarp();
