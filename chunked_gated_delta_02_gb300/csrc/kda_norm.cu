@@ -26,8 +26,7 @@ struct NormGateArgs {
   const __nv_bfloat16 *x, *gate;
   const float *weight;
   __nv_bfloat16 *y;
-  long long rows;
-  int inner;                       // rows per outer index
+  int rows, inner;                 // rows in all, rows per outer index
   long long xs[2], gs[2];          // strides in elements: outer, inner
   int D;
   float eps;
@@ -93,13 +92,17 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_gate_kernel(const 
   const int groups = blockDim.x / TPR;
   const int chunks = a.D / 8;
   const float inv_d = 1.0f / (float)a.D;
-  const long long row0 = (long long)blockIdx.x * (groups * U) + threadIdx.x / TPR;
+  const unsigned row0 = blockIdx.x * (groups * U) + threadIdx.x / TPR;   // rows < 2^31: no overflow
   uint4 xr[U][C], gr[U][C];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const long long row = row0 + (long long)u * groups;
-    if (row >= a.rows) continue;
-    const long long i = row / a.inner, j = row % a.inner;
+    const unsigned row = row0 + u * groups;
+    if (row >= (unsigned)a.rows) continue;
+    unsigned i = row, j = 0;
+    if (a.inner > 1) {   // 32-bit: a 64-bit division costs more than the rest of the row
+      i = row / (unsigned)a.inner;
+      j = row % (unsigned)a.inner;
+    }
     const uint4 *x = reinterpret_cast<const uint4 *>(a.x + i * a.xs[0] + j * a.xs[1]);
     const uint4 *g = reinterpret_cast<const uint4 *>(a.gate + i * a.gs[0] + j * a.gs[1]);
 #pragma unroll
@@ -111,8 +114,8 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_gate_kernel(const 
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const long long row = row0 + (long long)u * groups;
-    const bool live = row < a.rows;
+    const unsigned row = row0 + u * groups;
+    const bool live = row < (unsigned)a.rows;
     float s = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_gate_kernel(const 
     s = row_sum<TPR>(s, part);
     const float r = rsqrtf(fmaf(s, inv_d, a.eps));
     if (!live) continue;
-    uint4 *y = reinterpret_cast<uint4 *>(a.y + row * a.D);
+    uint4 *y = reinterpret_cast<uint4 *>(a.y + (long long)row * a.D);
 #pragma unroll
     for (int c = 0; c < C; ++c)
       if (c * TPR + t < chunks) {
@@ -245,7 +248,8 @@ constexpr int kAnyMaxD = 32768;   // 128 KiB of shared memory
 __global__ void __launch_bounds__(kAnyThreads) norm_gate_any_kernel(const NormGateArgs a) {
   extern __shared__ float row_buf[];
   __shared__ float part[kAnyThreads / 32];
-  const long long row = blockIdx.x, i = row / a.inner, j = row % a.inner;
+  const long long row = blockIdx.x;
+  const unsigned i = blockIdx.x / (unsigned)a.inner, j = blockIdx.x % (unsigned)a.inner;
   const __nv_bfloat16 *x = a.x + i * a.xs[0] + j * a.xs[1], *g = a.gate + i * a.gs[0] + j * a.gs[1];
   float s = 0.f;
   for (int k = threadIdx.x; k < a.D; k += kAnyThreads) {
@@ -318,11 +322,11 @@ static cudaError_t launch_norm_gate(const NormGateArgs &a, cudaStream_t s, int s
   constexpr int kThreads = TPR > 32 ? TPR : 256, kGroups = kThreads / TPR;
   if constexpr (TPR <= 32) {
     // Four rows per group only when that still leaves eight CTAs per SM.
-    if (a.rows >= (long long)sms * 8 * kGroups * 4)
-      return launch_kernel(norm_gate_kernel<TPR, C, 4>, dim3((unsigned)((a.rows + kGroups * 4 - 1) / (kGroups * 4))),
+    if (a.rows >= sms * 8 * kGroups * 4)
+      return launch_kernel(norm_gate_kernel<TPR, C, 4>, dim3(((unsigned)a.rows + kGroups * 4 - 1) / (kGroups * 4)),
                            dim3(kThreads), 0, s, false, a);
   }
-  return launch_kernel(norm_gate_kernel<TPR, C, 1>, dim3((unsigned)((a.rows + kGroups - 1) / kGroups)),
+  return launch_kernel(norm_gate_kernel<TPR, C, 1>, dim3(((unsigned)a.rows + kGroups - 1) / kGroups),
                        dim3(kThreads), 0, s, false, a);
 }
 
@@ -405,7 +409,7 @@ kda_status_t kda_norm_gate(const void *x, const void *gate, const float *weight,
   a.gate = static_cast<const __nv_bfloat16 *>(gate);
   a.weight = weight;
   a.y = static_cast<__nv_bfloat16 *>(y);
-  a.rows = outer * inner;
+  a.rows = (int)(outer * inner);
   a.inner = (int)inner;
   a.xs[0] = st[0]; a.xs[1] = st[1];
   a.gs[0] = st[2]; a.gs[1] = st[3];
