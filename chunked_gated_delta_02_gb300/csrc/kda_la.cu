@@ -1153,10 +1153,12 @@ kda_status_t kda_la_fwd(const void *q, const void *k, const void *v, const float
       if (n > 1 && (s3[x][i] <= 0 || s3[x][i] % 8 != 0 || s3[x][i] >= (int64_t)1 << 39)) return KDA_ERR_INVALID_ARG;
     }
   }
-  if ((double)B * T * H * std::max(K, V) > 9.0e15 || (double)num_seqs * H > 2.0e9) return KDA_ERR_UNSUPPORTED;
-  if (num_seqs == 0) return KDA_OK;
+  // Token positions, and work items a little past their number, are counted in 32 bits.
+  if ((double)B * T * H * std::max(K, V) > 9.0e15 || T > 2147480000) return KDA_ERR_UNSUPPORTED;
   const bool varlen = cu_seqlens != nullptr;
   const LaPlan pl = la_plan(T, H, K, V, num_seqs, varlen);
+  if ((double)std::max(pl.slots, (long long)num_seqs) * H > 2.0e9) return KDA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return KDA_OK;
   const LaScratch L = la_scratch(pl, H, K, V, num_seqs, varlen);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void *ws = workspace;

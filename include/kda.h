@@ -407,8 +407,9 @@ KDA_API kda_status_t kda_step(const void *q, const void *k, const void *v, const
  *   workspace      kda_la_workspace_size() bytes, 256-byte aligned, or NULL to
  *                  let the call allocate it stream-ordered where it needs any.
  *
- * K and V in {64, 128}; T may be 0. Alignment: q, k, v, o and the states 16
- * bytes, the rest its element size. A malformed cu_seqlens is reported as by
+ * K and V in {64, 128}; T may be 0. Calls of more than about 2^31 tokens per
+ * row, or of 10^9 (sequence, head) pairs, get KDA_ERR_UNSUPPORTED. Alignment:
+ * q, k, v, o and the states 16 bytes, the rest its element size. A malformed cu_seqlens is reported as by
  * kda_fwd(), and nothing is written. Repeated calls give the same bits.
  * Token values past a sequence's end, and those of other sequences, never reach
  * its results, be they infinite or NaN; within a sequence a non-finite k or v

@@ -129,6 +129,14 @@ def test_add_norm_refusals(lib, kw, code):
     assert add_norm(lib, **kw) == code
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=1 << 30, N=1 << 30, H=64), dict(T=2147483647), dict(T=2147480001),
+    dict(cu=FAKE, N=500_000_001, H=2), dict(cu=FAKE, N=1_000_000_001, H=1),
+])
+def test_la_fwd_refuses_more_than_it_counts_in_32_bits(lib, kw):
+    assert la_fwd(lib, **kw) == UNSUPPORTED
+
+
 def test_empty_calls_are_no_ops(lib):
     assert step(lib, N=0, q=None, k=None, v=None, beta=None, o=None) == OK
     assert la_step(lib, N=0, q=None, k=None, v=None, o=None) == OK
