@@ -90,6 +90,9 @@ struct LaMisc {
   uint64_t bar_exit;
   uint32_t tmem_slot;
   int err;
+  // this CTA's place among the others; its one item past the whole rounds, if it has one; the first chunk of
+  // item cta - 1, and the end of item cta, that it does
+  int cta, extra, cut0, cut1;
 };
 
 template <int K, int V, bool AGG>
@@ -134,6 +137,7 @@ __device__ __forceinline__ LaItem la_item(const LaProblem &p, int idx) {
     it.slot = idx;
     it.seg = g;
     it.n_seg = p.n_seg;
+    it.part = 0;
   }
   return it;
 }
@@ -209,8 +213,9 @@ __device__ __forceinline__ long long la_seg_index(int half, int v, int j) {
 }
 
 // AGG: only the state that each segment adds, started from zero (segments before the last of their
-// sequence). Otherwise everything, from the segment's start state.
-template <int K, int V, bool AGG>
+// sequence). Otherwise everything, from the segment's start state. SHARE: CTAs share items (below); a
+// kernel of its own, because in the one for short items what it adds cost 1 us per item.
+template <int K, int V, bool AGG, bool SHARE>
 __global__ void __launch_bounds__(kLaThreads, 1)
 la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
   using Lay = LaLayout<K, V, AGG>;
@@ -229,6 +234,24 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
   const int total = (p.cu ? p.counts[AGG ? 1 : 0] : p.N * p.n_seg) * p.H;   // below 2^31 (kda_la_fwd)
   if (total == 0) return;
 
+  // With R whole rounds of G CTAs and x more items, a CTA's even share is R + x / G items. CTA
+  // c begins with the first chunks of item c, goes on with items c + G, c + 2 G, ..., one of the x more where
+  // c x / G passes a whole number, and ends with the chunks of item c - 1 that CTA c - 1 left: where that one
+  // stopped makes all shares even. A state is thus handed over long after it was formed, and only by a CTA
+  // that started earlier: places are given in the order of starts.
+  if (SHARE && tid == 32) {
+    const int cta = atomicAdd(p.started, 1), G = gridDim.x, x = total % G;
+    const int e0 = (cta * x + G - 1) / G, e1 = ((cta + 1) * x + G - 1) / G;   // of the x, before and through this CTA
+    int cut[2];
+    for (int i = 0; i < 2; ++i) {
+      const int n = p.seg_chunks, left = (int)((long long)n * ((i ? e1 : e0) * G - (cta + i) * x) / G);
+      cut[i] = left < 2 ? n : n - left < 2 ? 0 : n - left;   // (handing over costs about a chunk's time)
+    }
+    ms.cta = cta;
+    ms.extra = e1 > e0 ? total - x + e0 : -1;
+    ms.cut0 = cut[0];
+    ms.cut1 = cut[1];
+  }
   if (warp == 0) {
     umma::tmem_alloc(&ms.tmem_slot, kLaTmemCols);
     umma::tmem_relinquish();
@@ -298,16 +321,31 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
   // f(item, head, n): every chunk of this CTA's items, n counting them over all items; begin(item,
   // head, chunks) and end(item, head, chunks) around them. All stop at the first false.
   auto for_chunks = [&](auto &&begin, auto &&chunk, auto &&end) {
-    // The items come longest first: rounds of one item per CTA, every other round backwards, even out
-    // what the CTAs get.
+    // Rounds of one item per CTA: neighbouring heads at the same time, whose tokens are neighbours in memory.
+    // Where none are shared, the items come longest first, and every other round goes backwards, to even
+    // out what the CTAs get.
     int n = 0;
-    const int ctas = gridDim.x, cta = blockIdx.x;
-    for (int first = 0, w0 = cta; first < total; first += ctas, w0 = ctas - 1 - w0) {
-      const int w = first + w0;
-      if (w >= total) continue;
-      const LaItem it = la_item(p, w / p.H);
+    const int ctas = gridDim.x, cta = SHARE ? ms.cta : (int)blockIdx.x, rounds = total / ctas;
+    for (int i = 0; i <= rounds + SHARE; ++i) {
+      int w = i * ctas + ((i & 1) && !SHARE ? ctas - 1 - cta : cta);
+      if (SHARE && i >= rounds) w = i == rounds ? ms.extra : cta - 1;
+      if (w < 0 || w >= total) continue;
+      LaItem it = la_item(p, w / p.H);
       const int h = w % p.H;
       if (AGG && it.seg == it.n_seg - 1) continue;
+      if constexpr (SHARE) {
+        if (i == 0 && it.len > ms.cut1 * kLaChunk) {
+          it.len = ms.cut1 * kLaChunk;
+          it.part = kLaToOther;
+        }
+        if (i > rounds) {
+          const int done = ms.cut0 * kLaChunk;
+          it.t0 += done;
+          it.len -= done;
+          it.part = done ? kLaFromOther : 0;
+        }
+        if (it.len <= 0) continue;
+      }
       const int nch = (it.len + kLaChunk - 1) / kLaChunk;
       if (!begin(it, h, nch)) return;
       for (int c = 0; c < nch; ++c, ++n)
@@ -708,18 +746,34 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
     // this warp's part of the copy's buffer, for the states' way to and from memory between items
     float *patch = reinterpret_cast<float *>(sm + Lay::s_off) + (half * (V / 32) + (warp & 3)) * (32 * (K / 4));
     auto seg_block = [&](int slot, int h) { return p.seg_state + ((long long)slot * p.H + h) * (K * V); };
+    // A state on its way from one CTA to the next, and this warp's flag for it
+    auto hand_block = [&](int cta) { return p.hand + (long long)cta * (K * V); };
+    auto hand_flag = [&](int cta) { return p.hand_there + cta * 8 + (warp - 8); };
+    auto hand_wait = [&](int cta) {
+      bool ok = true;
+      if (lane == 0) {
+        const unsigned t0 = (unsigned)clock();
+        while (ok && !umma::ld_acquire(hand_flag(cta))) {
+          if ((unsigned)clock() - t0 > kLaWaitLimit) *(volatile int *)&ms.err = 1;
+          ok = !*(volatile int *)&ms.err;
+        }
+      }
+      return (bool)__all_sync(0xffffffffu, ok);
+    };
     for_chunks(
         [&](const LaItem &it, int h, int nch) {
-          if (AGG || (it.seg == 0 && !p.init) || !has_v) {
+          const bool other = SHARE && (it.part & kLaFromOther);
+          if (AGG || (it.seg == 0 && !p.init && !other) || !has_v) {
 #pragma unroll
             for (int j = 0; j < KH; ++j) S[j] = 0.f;
-          } else if (it.seg == 0) {
+          } else if (it.seg == 0 && !other) {
             la_state_move<K, V, KH, false>(p, it.seq, h, (warp & 3) * 32, half * KH, S, patch);
           } else {
-            const float *src = seg_block(it.slot - 1, h);
+            if (other && !hand_wait(ms.cta - 1)) return false;
+            const float *src = other ? hand_block(ms.cta - 1) : seg_block(it.slot - 1, h);
 #pragma unroll
             for (int j = 0; j < KH / 4; ++j) {
-              const float4 f = *reinterpret_cast<const float4 *>(src + la_seg_index<K, V>(half, row, j));
+              const float4 f = __ldcg(reinterpret_cast<const float4 *>(src + la_seg_index<K, V>(half, row, j)));
               S[4 * j] = f.x; S[4 * j + 1] = f.y; S[4 * j + 2] = f.z; S[4 * j + 3] = f.w;
             }
           }
@@ -803,13 +857,19 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
         },
         [&](const LaItem &it, int h, int) {
           if (!has_v) return true;
-          if constexpr (AGG) {
-            float *dst = seg_block(it.slot, h);
+          if (AGG || (SHARE && (it.part & kLaToOther))) {
+            float *dst = AGG ? seg_block(it.slot, h) : hand_block(ms.cta);
 #pragma unroll
             for (int j = 0; j < KH / 4; ++j)
               *reinterpret_cast<float4 *>(dst + la_seg_index<K, V>(half, row, j)) =
                   make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
-            if (tid == 8 * 32) p.seg_decay[(long long)it.slot * p.H + h] = seg_decay;
+            if constexpr (AGG) {
+              if (tid == 8 * 32) p.seg_decay[(long long)it.slot * p.H + h] = seg_decay;
+            } else {
+              __threadfence();
+              __syncwarp();
+              if (lane == 0) umma::st_release(hand_flag(ms.cta), 1);
+            }
           } else if (it.seg == it.n_seg - 1 && p.final_state) {
             la_state_move<K, V, KH, true>(p, it.seq, h, (warp & 3) * 32, half * KH, S, patch);
           }
@@ -877,6 +937,12 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const LaProblem p) {
       }
     }
   }
+}
+
+// Clears the flags of the states handed over and the count of started CTAs.
+__global__ void __launch_bounds__(256) la_clear_kernel(int32_t *flags, int n) {
+  pdl_launch_dependents();
+  for (int i = threadIdx.x; i < n; i += 256) flags[i] = 0;
 }
 
 // Varlen schedule: checks cu_seqlens, cuts the sequences into segments of seg_chunks chunks and lists
@@ -978,7 +1044,7 @@ __global__ void __launch_bounds__(kLaSchedThreads) la_schedule_kernel(const LaPr
       it.slot = slot0 + g;
       it.t0 = g ? t0 + g * seg_len : t0;
       it.len = g < n - 1 ? seg_len : len - (it.t0 - t0);
-      it.pad = 0;
+      it.part = 0;
       // (a sequence's segments before its last have slot0 - i segments formed ahead before them)
       const int pos = g < n - 1 ? slot0 - i + g : atomicAdd(&s_bins[bin_of(nc - (n - 1) * p.seg_chunks)], 1);
       p.items[pos] = it;
@@ -995,7 +1061,11 @@ struct LaPlan {
   long long slots;
   bool segments;       // whether any sequence may have more than one segment
   long long multi;     // how many may
+  int shared;          // CTAs of a call that may hand a state over, or 0
 };
+
+// CTAs share items where one of them would else have more than this many chunks over its share.
+constexpr int kLaShareChunks = 3;
 
 // Time model of a call, in microseconds: `rounds` of items of `chunks` chunks each per CTA, in the
 // kernel that does everything and in the one that forms the segments' states. The constants were
@@ -1003,23 +1073,25 @@ struct LaPlan {
 // the memory bandwidth.
 constexpr double kLaChunkUs = 2.6, kLaAggChunkUs = 1.9, kLaItemUs = 2.0, kLaPassUs = 7.0, kLaBytesPerUs = 6.5e6;
 
-static double la_pass_us(long long items, int chunks, int sms, double chunk_us, double chunk_bytes) {
+static double la_pass_us(long long items, int chunks, int sms, double chunk_us, double chunk_bytes, bool share) {
   if (items == 0) return 0.0;
-  const long long rounds = (items + sms - 1) / sms;
+  double rounds = (double)((items + sms - 1) / sms);
+  if (share && (rounds - (double)items / sms) * chunks > kLaShareChunks)
+    rounds = std::max(1.0, (double)items / sms + (double)kLaShareChunks / chunks);
   const double mem_us = chunk_bytes * (double)std::min(items, (long long)sms) / kLaBytesPerUs;
-  return (double)rounds * (chunks * std::max(chunk_us, mem_us) + kLaItemUs);
+  return rounds * (chunks * std::max(chunk_us, mem_us) + kLaItemUs);
 }
 
 // Chunks per segment of `chains` (sequence, head) pairs of nc chunks each: few chains leave SMs idle,
-// and cutting them into segments costs a pass over k and v.
-static int la_segment_chunks(long long chains, int nc, int K, int V, int sms) {
+// and cutting them into segments costs a pass over k and v. share: whether CTAs may share items.
+static int la_segment_chunks(long long chains, int nc, int K, int V, int sms, bool share) {
   const double bytes = kLaChunk * 2.0 * (2 * K + 2 * V), agg_bytes = kLaChunk * 2.0 * (K + V);
   int best = nc;
-  double best_us = la_pass_us(chains, nc, sms, kLaChunkUs, bytes);
+  double best_us = la_pass_us(chains, nc, sms, kLaChunkUs, bytes, share);
   for (int n = 2; n <= 512 && n <= nc; ++n) {
     const int seg = (nc + n - 1) / n, m = (nc + seg - 1) / seg;
-    const double us = la_pass_us(chains * m, seg, sms, kLaChunkUs, bytes) +
-                      la_pass_us(chains * (m - 1), seg, sms, kLaAggChunkUs, agg_bytes) + kLaPassUs;
+    const double us = la_pass_us(chains * m, seg, sms, kLaChunkUs, bytes, share) +
+                      la_pass_us(chains * (m - 1), seg, sms, kLaAggChunkUs, agg_bytes, false) + kLaPassUs;
     if (us < 0.95 * best_us) {
       best_us = us;
       best = seg;
@@ -1029,22 +1101,24 @@ static int la_segment_chunks(long long chains, int nc, int K, int V, int sms) {
 }
 
 static LaPlan la_plan(int T, int H, int K, int V, int N, bool varlen) {
-  LaPlan r;
+  LaPlan r = {};
   const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
   const int nc = std::max(1, (int)(((long long)T + kLaChunk - 1) / kLaChunk));
   if (!varlen) {
-    r.seg_chunks = la_segment_chunks((long long)N * H, nc, K, V, sms);
+    r.seg_chunks = la_segment_chunks((long long)N * H, nc, K, V, sms, true);
     r.n_seg = (nc + r.seg_chunks - 1) / r.seg_chunks;
     r.segments = r.n_seg > 1;
     r.slots = (long long)N * r.n_seg;
     r.multi = N;
+    const long long items = r.slots * H, rounds = (items + sms - 1) / sms;
+    if (items > sms && (rounds - (double)items / sms) * r.seg_chunks > kLaShareChunks) r.shared = sms;
     return r;
   }
   // The lengths are on the device: segments as for equal lengths, and never longer than what an SM has
   // to do on average, so that one long sequence among short ones does not hold up the call.
   const int nc_mean = std::max(1, (int)(((long long)T / std::max(N, 1) + kLaChunk - 1) / kLaChunk));
   const int share = (int)std::min((double)nc, std::ceil((nc + 0.5 * N) * (double)H / sms));
-  r.seg_chunks = la_segment_chunks((long long)N * H, nc_mean, K, V, sms);
+  r.seg_chunks = la_segment_chunks((long long)N * H, nc_mean, K, V, sms, false);
   if (r.seg_chunks >= nc_mean) r.seg_chunks = std::max(nc_mean, std::max(share, 8));
   r.n_seg = 1;
   r.multi = std::min((long long)N, (long long)T / ((long long)r.seg_chunks * kLaChunk));
@@ -1054,7 +1128,7 @@ static LaPlan la_plan(int T, int H, int K, int V, int N, bool varlen) {
 }
 
 struct LaScratch {
-  size_t flag, counts, slot0, multi, items, decay, state, total;
+  size_t flag, counts, slot0, multi, items, decay, state, hand, there, total;
 };
 static LaScratch la_scratch(const LaPlan &pl, int H, int K, int V, int N, bool varlen) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -1077,21 +1151,27 @@ static LaScratch la_scratch(const LaPlan &pl, int H, int K, int V, int N, bool v
     s.state = off;
     off = up(off + 4 * (size_t)pl.slots * H * K * V);
   }
+  if (pl.shared) {
+    s.there = off;   // and after the flags the count of started CTAs
+    off = up(off + 4 * (8 * (size_t)pl.shared + 1));
+    s.hand = off;
+    off = up(off + 4 * (size_t)pl.shared * K * V);
+  }
   s.total = off;
   return s;
 }
 
-template <int K, int V, bool AGG>
+template <int K, int V, bool AGG, bool SHARE = false>
 static cudaError_t launch_la_t(const LaProblem &p, const LaMaps &maps, long long items, cudaStream_t stream, bool overlap) {
   static PerDeviceOnce attr;
   constexpr int smem = (int)LaLayout<K, V, AGG>::bytes;
   cudaError_t e = attr([&](int) {
-    return cudaFuncSetAttribute(la_kernel<K, V, AGG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(la_kernel<K, V, AGG, SHARE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (e != cudaSuccess) return e;
   const int sms = device_sm_count();
   const long long grid = std::min(items * p.H, (long long)(sms > 0 ? sms : 1));
-  return launch_kernel(la_kernel<K, V, AGG>, dim3((unsigned)grid), dim3(kLaThreads), smem, stream, overlap, p, maps);
+  return launch_kernel(la_kernel<K, V, AGG, SHARE>, dim3((unsigned)grid), dim3(kLaThreads), smem, stream, overlap, p, maps);
 }
 
 template <int K, int V>
@@ -1102,6 +1182,11 @@ static cudaError_t launch_la(const LaProblem &p, const LaMaps &maps, const LaPla
     const cudaError_t e = launch_kernel(la_schedule_kernel, dim3(1), dim3(kLaSchedThreads), 0, s, false, p);
     if (e != cudaSuccess) return e;
   }
+  if (pl.shared) {
+    const cudaError_t e = launch_kernel(la_clear_kernel, dim3(1), dim3(256), 0, s, false, p.hand_there, 8 * pl.shared + 1);
+    if (e != cudaSuccess) return e;
+    overlap = true;
+  }
   if (pl.segments) {
     cudaError_t e = launch_la_t<K, V, true>(p, maps, items, s, overlap);
     if (e == cudaSuccess)
@@ -1109,7 +1194,8 @@ static cudaError_t launch_la(const LaProblem &p, const LaMaps &maps, const LaPla
     if (e != cudaSuccess) return e;
     overlap = true;
   }
-  return launch_la_t<K, V, false>(p, maps, items, s, overlap);
+  return pl.shared ? launch_la_t<K, V, false, true>(p, maps, items, s, overlap)
+                   : launch_la_t<K, V, false>(p, maps, items, s, overlap);
 }
 
 static bool la_sizes_ok(int B, int T, int Hk, int H, int K, int V, int N) {
@@ -1189,6 +1275,11 @@ kda_status_t kda_la_fwd(const void *q, const void *k, const void *v, const float
   if (pl.segments) {
     p.seg_decay = reinterpret_cast<float *>(base + L.decay);
     p.seg_state = reinterpret_cast<float *>(base + L.state);
+  }
+  if (pl.shared) {
+    p.hand = reinterpret_cast<float *>(base + L.hand);
+    p.hand_there = reinterpret_cast<int32_t *>(base + L.there);
+    p.started = p.hand_there + 8 * pl.shared;
   }
   p.scale = scale;
   p.B = B; p.T = T; p.Hk = Hk; p.H = H; p.N = num_seqs;

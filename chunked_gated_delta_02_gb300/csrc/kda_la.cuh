@@ -14,8 +14,10 @@ struct LaItem {
   int b;
   int slot;           // index of its segment among all segments
   int seg, n_seg;     // segment of the sequence, number of them
-  int pad;
+  int part;           // while a CTA has it: kLaFromOther, kLaToOther
 };
+// The CTA before does the item's first chunks; the CTA after this, its last ones.
+constexpr int kLaFromOther = 1, kLaToOther = 2;
 
 struct LaProblem {
   const float *decay;            // log decay, [H] or per token (kLaTokenDecay)
@@ -36,6 +38,11 @@ struct LaProblem {
   int32_t *counts;
   int32_t *slot0;
   int32_t *multi;
+  // Items that two CTAs share (fixed length): the state at the end of CTA c's part at hand + c K V, and for
+  // each of its state warps whether it is there; how many CTAs have started. Null where none are shared.
+  float *hand;
+  int32_t *hand_there;           // [CTAs][8]
+  int32_t *started;
   int32_t *flag;                 // per-call data-error flag (varlen) or null
   int *dev_status;
   float scale;

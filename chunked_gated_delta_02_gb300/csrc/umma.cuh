@@ -301,6 +301,14 @@ __device__ __forceinline__ uint32_t mbar_try_wait(uint64_t *bar, uint32_t parity
   return ok;
 }
 // Whether phase `parity` of `bar` is complete, without suspending the thread.
+__device__ __forceinline__ int ld_acquire(const int *p) {
+  int x;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+  return x;
+}
+__device__ __forceinline__ void st_release(int *p, int x) {
+  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(x) : "memory");
+}
 __device__ __forceinline__ uint32_t mbar_test(uint64_t *bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(

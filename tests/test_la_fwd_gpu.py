@@ -108,6 +108,26 @@ def test_segments_of_long_sequences(lens, init):
     check(d, f"segments {lens}")
 
 
+@pytest.mark.parametrize("K,V", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("lens,H", [([1250] * 5, 40), ([1250] * 51, 3), ([900, 0, 2047, 1, 513, 1400, 130, 1664, 700, 1025], 24),
+                                    ([600] * 40 + [3000, 512], 5)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_sequences_shared_by_two_blocks(lens, H, K, V, packed):
+    """More sequences and heads than SMs, and not a multiple: their chunks are dealt out evenly, so that a
+    block goes on with the state of another."""
+    if packed:
+        d = make(1, 0, H, H, K, V, seed=H + K, lens=lens, token=True)
+    elif len(set(lens)) > 1:
+        pytest.skip("packed only")
+    else:
+        d = make(len(lens), lens[0], H, H, K, V, seed=H + K, init=None)
+    first = check(d, f"{len(lens)} x {H}")
+    for _ in range(3):
+        again = kda.la_fwd(d["q"], d["k"], d["v"], d["log_decay"], initial_state=d["initial_state"],
+                           output_final_state=True, cu_seqlens=d["cu_seqlens"])
+        assert all(torch.equal(x, y) for x, y in zip(first, again))
+
+
 @pytest.mark.parametrize("decay", [0.0, -1e-4, -0.7, -5.0, -60.0, float("-inf")])
 @pytest.mark.parametrize("T", [200, 4500])
 def test_constant_decays(decay, T):
