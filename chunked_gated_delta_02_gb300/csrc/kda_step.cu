@@ -9,12 +9,18 @@
 // For KDA the output needs no second pass over S': o = scale (s^T qhat + (qhat . khat) u), so both
 // products s^T khat and s^T qhat are formed in one sweep and S' is written from registers.
 //
-// Bound: the state is read and written once, 128 KiB per request and head at K = V = 128 in fp32,
-// against about 1 KiB of token data and 7 K V operations: memory bandwidth. A CTA of 128 threads
-// takes a 16 KiB tile of one state (whole rows of the contiguous dimension's 128 bytes per 8
-// lanes), and issues all loads of the tile before it computes anything: the gate, the norms and
-// the block reduction run while the tile is in flight. Small batches (N H < SM count) still give
-// V / 32 CTAs per state.
+// Bound: the state is read and written once, 128 KiB per request and head at K = V = 128 in fp32, against
+// about 1 KiB of token data and 7 K V operations: memory bandwidth. A CTA of 128 threads takes a 16 KiB
+// tile of one state (8 KiB of bf16 at K = 64). It issues the token's loads together with that of the row
+// index, all loads of the tile as soon as the index is there, and only then computes anything: the gate,
+// the norms and the block reduction run while the tile is in flight. Small batches (N H < SM count) still
+// give V / 32 CTAs per fp32 state.
+//
+// Measured for 200 requests of 32 heads, K = V = 128, microseconds and the share of the copy bandwidth of
+// 6.78 TB/s: fp32 KDA 124.8 (100%) and, [K, V] layout, 126.6 (99%), linear attention 124.0 (100%); bf16 KDA
+// 70.0 (90%) and 78.1 (81%). With the token's loads after the tile's, fp32 [K, V] took 137 and four
+// requests 7.2 us instead of 6.0. Where bf16 states leave bandwidth unused, it is the fixed work per CTA:
+// 400 requests at K = V = 64 take 45.8 us (70%), and halving the tile at K = 128 made 90 us of 72.
 #include <cmath>
 #include <cstring>
 
@@ -88,28 +94,34 @@ __device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
 // Tile of one CTA: R rows x CB columns of the stored matrix, CB along the contiguous dimension.
 //   [V, K] layout: rows are value columns v, a row holds all K channels (CB = K);
 //   [K, V] layout: rows are all K channels, CB value columns (128 bytes).
-// 8 lanes cover 128 bytes of a row, a warp 4 rows, the CTA 16 rows per pass.
-template <int K, typename ST, bool KV>
+// 8 lanes cover 128 bytes of a row at a time, a warp 4 rows, the CTA 16 rows per pass. A bf16 row of KDA at
+// K = 128 is covered by 16 lanes at once: 8 would hold the three factors of 16 channels each, which leaves
+// registers for four CTAs per SM (72.6 us; 16 lanes and seven CTAs 69.5 us, 16 lanes and four 72.5).
+template <bool KDA, int K, typename ST, bool KV>
 struct StepTile {
   static constexpr int vec = StateVec<ST>::n;
-  static constexpr int span = 8 * vec;                                   // values of 8 lanes: 128 bytes
+  static constexpr int lanes = (KDA && !KV && K == 128 && vec == 8) ? 16 : 8;         // of a row
+  static constexpr int span = lanes * vec;                               // values that they load at a time
   static constexpr int cols = KV ? span : K;
   static constexpr int per_row = cols / span;                            // 16-byte loads per lane and row
   static constexpr int rows = KV ? K : (per_row == 4 ? 32 : 64);
-  static constexpr int passes = rows / (4 * kStepWarps);
+  static constexpr int pass_rows = kStepThreads / lanes;
+  static constexpr int passes = rows / pass_rows;
   static constexpr int slice = KV ? cols : rows;                         // value columns per CTA
 };
 
-// CTAs per SM the registers are fitted to. Six keep 96 KiB of loads in flight. KDA on a bf16 state has
-// twice the values per byte and their three factors to hold: fitted to six it spills and takes 110.7 us
-// for 200 requests of 32 heads at K = V = 128, fitted to four 74.4 us (floor 63.1 us; fp32 state, six:
-// 124.4 us, floor 125.0 us).
-template <bool KDA, typename ST>
-constexpr int kStepCtas = (KDA && sizeof(ST) == 2) ? 4 : 6;
+// CTAs per SM the registers are fitted to: six keep 96 KiB of loads in flight, as much as an fp32 state
+// needs (124.4 us of 125.0). bf16 states have twice the values per byte to work on, and more or fewer CTAs
+// pay, as long as nothing spills (microseconds at 200 requests of 32 heads, K = 64: 400, V = 64): linear
+// attention at K = 64 ten, 35.5 (six 37.6, twelve 37.4); KDA at K = 64 six, 45.8 (five 49.1, seven 46.1),
+// at K = 128 seven, 70.0 (six 70.7, eight 74.5), and in the [K, V] layout, where it spills from five on,
+// four, 78.1 (five 81.2, seven 95.8).
+template <bool KDA, int K, typename ST, bool KV>
+constexpr int kStepCtas = sizeof(ST) == 4 ? 6 : KDA ? (K == 64 ? 6 : KV ? 4 : 7) : K == 64 ? 10 : 6;
 
 template <bool KDA, int K, typename ST, bool KV>
-__global__ void __launch_bounds__(kStepThreads, kStepCtas<KDA, ST>) step_kernel(const StepArgs a) {
-  using T = StepTile<K, ST, KV>;
+__global__ void __launch_bounds__(kStepThreads, kStepCtas<KDA, K, ST, KV>) step_kernel(const StepArgs a) {
+  using T = StepTile<KDA, K, ST, KV>;
   using Vec = StateVec<ST>;
   constexpr int kVec = T::vec;
   __shared__ __align__(16) float s_q[K], s_k[K], s_a[K], s_v[T::slice];
@@ -123,12 +135,36 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<KDA, ST>) step_kernel(
   const int n = nh / a.H, h = nh % a.H;
   __nv_bfloat16 *o = a.o + (long long)nh * a.V + v0;
   const long long row = a.idx ? (long long)a.idx[n] : (long long)n;
+
+  // ---- token data, on its way while the row index is (and converted only later: a use would wait for it):
+  // channel tid of q, k and the gate; value column tid of the slice
+  __nv_bfloat16 q_raw = {}, k_raw = {}, v_raw = {}, g_raw = {}, beta_raw = {};
+  float beta = 0.f, log_decay = 0.f, dt = 0.f, A_log = 0.f;
+  if (tid < K) {
+    const int hk = h / a.group;
+    q_raw = a.q[n * a.qs[0] + hk * a.qs[1] + tid];
+    k_raw = a.k[n * a.ks[0] + hk * a.ks[1] + tid];
+    if constexpr (KDA) {
+      const bool per_head = a.flags & kGatePerHead;
+      g_raw = static_cast<const __nv_bfloat16 *>(a.g)[n * a.gs[0] + h * a.gs[1] + (per_head ? 0 : tid)];
+      if (a.dt_bias) dt = a.dt_bias[per_head ? h : h * K + tid];
+    }
+  }
+  if (tid < T::slice) v_raw = a.v[n * a.vs[0] + h * a.vs[1] + v0 + tid];
+  if constexpr (KDA) {
+    A_log = a.A_log[h];
+    const long long bi = n * a.bs[0] + h * a.bs[1];
+    if (a.flags & kBetaF32) beta = static_cast<const float *>(a.beta)[bi];
+    else beta_raw = static_cast<const __nv_bfloat16 *>(a.beta)[bi];
+  } else {
+    log_decay = static_cast<const float *>(a.g)[(a.flags & kLaTokenDecay) ? n * a.gs[0] + h * a.gs[1] : h];
+  }
   if (row < 0 || row >= a.num_states) {   // a padding entry, or an index outside the pool: no state is touched
     if (row >= a.num_states && tid == 0) atomicExch(a.dev_status, kDevBadStateIndex);
     if (tid < T::slice) o[tid] = __float2bfloat16_rn(0.f);
     return;
   }
-  const int c = lane & 7, r = warp * 4 + (lane >> 3);
+  const int c = lane % T::lanes, r = tid / T::lanes;
   ST *tile = static_cast<ST *>(a.state) + (row * a.H + h) * (long long)K * a.V + (KV ? v0 : (long long)v0 * K);
   const long long ld = KV ? a.V : K;
 
@@ -138,39 +174,29 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<KDA, ST>) step_kernel(
   for (int p = 0; p < T::passes; ++p)
 #pragma unroll
     for (int j = 0; j < T::per_row; ++j)
-      raw[p][j] = __ldcs(reinterpret_cast<const uint4 *>(tile + (p * 16 + r) * ld + j * T::span + c * kVec));
+      raw[p][j] = __ldcs(reinterpret_cast<const uint4 *>(tile + (p * T::pass_rows + r) * ld + j * T::span + c * kVec));
 
-  // ---- token data: channel tid of q, k and the decay; value column tid of the slice
   float sums[3] = {0.f, 0.f, 0.f};   // |q|^2, |k|^2, q . k
   if (tid < K) {
-    const int hk = h / a.group;
-    const float qv = __bfloat162float(a.q[n * a.qs[0] + hk * a.qs[1] + tid]);
-    const float kv = __bfloat162float(a.k[n * a.ks[0] + hk * a.ks[1] + tid]);
+    const float qv = __bfloat162float(q_raw), kv = __bfloat162float(k_raw);
     s_q[tid] = qv;
     s_k[tid] = kv;
     if constexpr (KDA) {
-      const bool per_head = a.flags & kGatePerHead;
-      const float g = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.g)[n * a.gs[0] + h * a.gs[1] + (per_head ? 0 : tid)]);
-      const float dt = a.dt_bias ? a.dt_bias[per_head ? h : h * K + tid] : 0.f;
-      s_a[tid] = ex2_approx(log2_decay(g, dt, ex2_approx(a.A_log[h] * kLog2e), a.lb * kLog2e));
+      s_a[tid] = ex2_approx(log2_decay(__bfloat162float(g_raw), dt, ex2_approx(A_log * kLog2e), a.lb * kLog2e));
       sums[0] = qv * qv;
       sums[1] = kv * kv;
       sums[2] = qv * kv;
     }
   }
-  if (tid < T::slice) s_v[tid] = __bfloat162float(a.v[n * a.vs[0] + h * a.vs[1] + v0 + tid]);
-  float beta = 1.f, decay = 1.f;
+  if (tid < T::slice) s_v[tid] = __bfloat162float(v_raw);
+  const float decay = KDA ? 1.f : ex2_approx(log_decay * kLog2e);
   if constexpr (KDA) {
-    const long long bi = n * a.bs[0] + h * a.bs[1];
-    beta = sigmoid_fast((a.flags & kBetaF32) ? static_cast<const float *>(a.beta)[bi]
-                                             : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.beta)[bi]));
+    beta = sigmoid_fast((a.flags & kBetaF32) ? beta : __bfloat162float(beta_raw));
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       sums[i] = warp_sum(sums[i]);
       if (lane == 0) s_part[i][warp] = sums[i];
     }
-  } else {
-    decay = ex2_approx(static_cast<const float *>(a.g)[(a.flags & kLaTokenDecay) ? n * a.gs[0] + h * a.gs[1] : h] * kLog2e);
   }
   __syncthreads();
   float rq = 1.f, rk = 1.f, qk = 0.f;   // norm factors of q and k, and qhat . khat
@@ -200,7 +226,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<KDA, ST>) step_kernel(
     }
 #pragma unroll
     for (int p = 0; p < T::passes; ++p) {
-      const int vi = p * 16 + r;
+      const int vi = p * T::pass_rows + r;
       const float vv = s_v[vi];
       float2 x[T::per_row][kPairs];
       float2 d1 = splat(0.f), d2 = splat(0.f);
@@ -220,7 +246,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<KDA, ST>) step_kernel(
       }
       float s1 = d1.x + d1.y, s2 = d2.x + d2.y;
 #pragma unroll
-      for (int m = 1; m < 8; m <<= 1) {
+      for (int m = 1; m < T::lanes; m <<= 1) {
         if constexpr (KDA) s1 += __shfl_xor_sync(0xffffffffu, s1, m);
         s2 += __shfl_xor_sync(0xffffffffu, s2, m);
       }
@@ -246,7 +272,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<KDA, ST>) step_kernel(
     for (int e = 0; e < kPairs; ++e) d1[e] = d2[e] = splat(0.f);
 #pragma unroll
     for (int p = 0; p < T::passes; ++p) {
-      const int k = p * 16 + r;
+      const int k = p * T::pass_rows + r;
       const float2 kk = splat(s_k[k]), qq = splat(s_q[k]);
       float2 x[kPairs];
       Vec::unpack(raw[p][0], x);
@@ -296,7 +322,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<KDA, ST>) step_kernel(
       }
 #pragma unroll
       for (int p = 0; p < T::passes; ++p) {
-        const int k = p * 16 + r;
+        const int k = p * T::pass_rows + r;
         const float2 kk = splat(s_k[k]), aa = splat(s_a[k]);
         float2 x[kPairs];
         Vec::unpack(raw[p][0], x);
@@ -320,7 +346,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas<KDA, ST>) step_kernel(
 
 template <bool KDA, int K, typename ST, bool KV>
 static cudaError_t launch_step_t(const StepArgs &a, cudaStream_t stream) {
-  const long long grid = (long long)a.N * a.H * (a.V / StepTile<K, ST, KV>::slice);
+  const long long grid = (long long)a.N * a.H * (a.V / StepTile<KDA, K, ST, KV>::slice);
   return launch_kernel(step_kernel<KDA, K, ST, KV>, dim3((unsigned)grid), dim3(kStepThreads), 0, stream, false, a);
 }
 
