@@ -38,11 +38,13 @@
 // which a thread can update its part of S^T and write it as rows of M2's operand without transposing.
 //
 // Bound: a chunk of one head moves 128 KiB at K = V = 128, 2.9 us of an SM's share of the measured
-// bandwidth, against 48 tensor-core steps of 64 clocks, 1.6 us: memory bandwidth, if loads, products
-// and register work overlap. Shared memory holds two chunks, so a chunk's period is half the time from
-// the request of its tiles to their release: that time is kept short by forming V' and P in separate
-// warps and by releasing q, k and v on their own. (o leaves by the copy engine: stored by the state warps
-// it took 1400 clocks of their time from shared memory and 2700 from registers.)
+// bandwidth, against 48 tensor-core steps of 64 clocks, 1.6 us: memory bandwidth, where every SM has work.
+// Measured: 4 x 4096 tokens of 64 heads 187 us, 5.8 TB/s, 85% of the copy bandwidth. Alone on its SM a
+// chunk takes 2.75 us, whatever the other SMs do, and few sequences and heads are bound by that: scores ->
+// P -> O -> next scores and D -> S -> O -> next D are two loops of about 5200 clocks, of which the products
+// take 3100. What keeps them short: V' and P in separate warps; q, k and v released on their own; a state's
+// update or a chunk's output, whichever product is done first; o stored by the copy engine (by the state
+// warps it took 1400 clocks of their time from shared memory and 2700 from registers).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -1064,17 +1066,19 @@ struct LaPlan {
   int shared;          // CTAs of a call that may hand a state over, or 0
 };
 
-// CTAs share items where one of them would else have more than this many chunks over its share. Measured
-// on 152 SMs with K = V = 128, shared and whole items: 256 items of 8 chunks, 2.5 over, 70 and 66 us; 160
+// CTAs share items where one of them would else have more than this many chunks over its share. Measured on
+// 152 SMs with K = V = 128, shared and whole items: 256 items of 8 chunks, 2.5 over, 70 and 66 us; 160
 // items of 4, 3.8 over, 37.5 and 39.6; 256 of 16, 5 over, 108 and 111; 256 of 32, 10 over, 187 and 199; 192
 // of 128, 94 over, 518 and 754.
 constexpr int kLaShareChunks = 3;
 
-// Time model of a call, in microseconds: `rounds` of items of `chunks` chunks each per CTA, in the
-// kernel that does everything and in the one that forms the segments' states. The constants were
-// measured at K = V = 128 (one item per CTA, many chunks); a chunk takes at least its bytes' share of
-// the memory bandwidth.
-constexpr double kLaChunkUs = 2.6, kLaAggChunkUs = 1.9, kLaItemUs = 2.0, kLaPassUs = 7.0, kLaBytesPerUs = 6.5e6;
+// Time model of a call, in microseconds: rounds of items of `chunks` chunks each per CTA, in the kernel
+// that does everything and in the one that forms the segments' states. The constants were measured at K = V
+// = 128: 512 chunks in a row take 1407 us, and the segments of 65536 tokens of 16 heads, 57 chunks per CTA,
+// 88 us; an item adds 2 us, the second pass with its combine 12. A chunk takes at least its bytes' share of
+// the memory bandwidth. The number of segments it chooses is within 4% of the best of 24 that were tried
+// for each of 22 shapes (but 6% for 3 x 4096 tokens of 24 heads).
+constexpr double kLaChunkUs = 2.75, kLaAggChunkUs = 1.6, kLaItemUs = 2.0, kLaPassUs = 12.0, kLaBytesPerUs = 6.5e6;
 
 static double la_pass_us(long long items, int chunks, int sms, double chunk_us, double chunk_bytes, bool share) {
   if (items == 0) return 0.0;
