@@ -290,6 +290,10 @@ __device__ __forceinline__ uint32_t mbar_try_wait(uint64_t *bar, uint32_t parity
   return ok;
 }
 // Whether phase `parity` of `bar` is complete, without suspending the thread.
+// Asks for `bytes` (a multiple of 16) of global memory at the 16-byte aligned p to be brought into L2.
+__device__ __forceinline__ void prefetch_l2_bulk(const void *p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ int ld_acquire(const int *p) {
   int x;
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");

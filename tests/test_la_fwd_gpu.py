@@ -109,16 +109,15 @@ def test_segments_of_long_sequences(lens, init):
 
 
 @pytest.mark.parametrize("K,V", [(64, 64), (64, 128), (128, 64), (128, 128)])
-@pytest.mark.parametrize("lens,H", [([1250] * 5, 40), ([1250] * 51, 3), ([900, 0, 2047, 1, 513, 1400, 130, 1664, 700, 1025], 24),
-                                    ([600] * 40 + [3000, 512], 5)])
-@pytest.mark.parametrize("packed", [False, True])
-def test_sequences_shared_by_two_blocks(lens, H, K, V, packed):
-    """More sequences and heads than SMs, and not a multiple: their chunks are dealt out evenly, so that a
-    block goes on with the state of another."""
+@pytest.mark.parametrize("lens,H,packed", [
+    ([1250] * 5, 40, False), ([1250] * 51, 3, False), ([1250] * 5, 40, True), ([600] * 40 + [3000, 512], 5, True),
+    ([900, 0, 2047, 1, 513, 1400, 130, 1664, 700, 1025], 24, True),
+])
+def test_more_sequences_than_blocks(lens, H, packed, K, V):
+    """More sequences and heads than SMs, and not a multiple: where lengths are equal, a block goes on with
+    the state of another."""
     if packed:
         d = make(1, 0, H, H, K, V, seed=H + K, lens=lens, token=True)
-    elif len(set(lens)) > 1:
-        pytest.skip("packed only")
     else:
         d = make(len(lens), lens[0], H, H, K, V, seed=H + K, init=None)
     first = check(d, f"{len(lens)} x {H}")
