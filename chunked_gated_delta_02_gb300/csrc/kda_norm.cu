@@ -15,6 +15,9 @@
 // bandwidth; add_norm of 16384 rows of 4096 values, fp32 residual and all parts, 138 us, 100%; bf16 residual,
 // addition and norm alone, 82 us, 96%.
 //
+// Launches overlap the end of the kernel ahead in the stream: in a graph of calls on eight rows norm_gate takes
+// 1.6 us instead of 1.9, add_norm 2.35 instead of 2.7.
+//
 // Rows that do not fit the 16-byte path (D not a multiple of 8, an unaligned base or stride, or
 // more than 16384 values) take a CTA per row with element-wise loads and the row in shared memory.
 #include <cmath>
@@ -93,6 +96,7 @@ __device__ __forceinline__ float row_sum(float s, float *part) {
 template <int TPR, int C, int U>
 __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_gate_kernel(const NormGateArgs a) {
   __shared__ float part[TPR > 32 ? TPR / 32 : 1];
+  pdl_wait();
   const int t = threadIdx.x % TPR;
   const int groups = blockDim.x / TPR;
   const int chunks = a.D / 8;
@@ -170,6 +174,7 @@ template <int TPR, int C, typename RT>
 __global__ void __launch_bounds__(kNormBlock<TPR>, kAddNormThreads<TPR, C, RT> / kNormBlock<TPR>)
 add_norm_kernel(const AddNormArgs a, long long rows) {
   __shared__ float part[2][TPR > 32 ? TPR / 32 : 1];
+  pdl_wait();
   const int t = threadIdx.x % TPR;
   const int chunks = a.D / 8;
   const float inv_d = 1.0f / (float)a.D;
@@ -279,6 +284,7 @@ constexpr int kAnyMaxD = 32768;   // 128 KiB of shared memory
 __global__ void __launch_bounds__(kAnyThreads) norm_gate_any_kernel(const NormGateArgs a) {
   extern __shared__ float row_buf[];
   __shared__ float part[kAnyThreads / 32];
+  pdl_wait();
   const long long row = blockIdx.x;
   const unsigned i = blockIdx.x / (unsigned)a.inner, j = blockIdx.x % (unsigned)a.inner;
   const __nv_bfloat16 *x = a.x + i * a.xs[0] + j * a.xs[1], *g = a.gate + i * a.gs[0] + j * a.gs[1];
@@ -301,6 +307,7 @@ template <typename RT>
 __global__ void __launch_bounds__(kAnyThreads) add_norm_any_kernel(const AddNormArgs a) {
   extern __shared__ float row_buf[];
   __shared__ float part[2][kAnyThreads / 32];
+  pdl_wait();
   const long long row = blockIdx.x;
   const __nv_bfloat16 *x = a.x + row * a.xs, *g = a.gate ? a.gate + row * a.gs : nullptr;
   const RT *res = static_cast<const RT *>(a.residual) + row * a.rs;
@@ -356,10 +363,10 @@ static cudaError_t launch_norm_gate(const NormGateArgs &a, cudaStream_t s, int s
     // rows of 64 15.4 and 14.8.
     if (a.rows >= sms * 24 * kGroups * 4)
       return launch_kernel(norm_gate_kernel<TPR, C, 4>, dim3(((unsigned)a.rows + kGroups * 4 - 1) / (kGroups * 4)),
-                           dim3(kThreads), 0, s, false, a);
+                           dim3(kThreads), 0, s, true, a);
   }
   return launch_kernel(norm_gate_kernel<TPR, C, 1>, dim3(((unsigned)a.rows + kGroups - 1) / kGroups),
-                       dim3(kThreads), 0, s, false, a);
+                       dim3(kThreads), 0, s, true, a);
 }
 
 template <int TPR, int C, typename RT>
@@ -367,7 +374,7 @@ static cudaError_t launch_add_norm(AddNormArgs a, long long rows, cudaStream_t s
   constexpr int kThreads = kNormBlock<TPR>, kGroups = kThreads / TPR;
   a.ahead = (int)(kAddNormAheadBytes / (a.D * (2.0 + sizeof(RT) + (a.gate ? 2 : 0))));
   return launch_kernel(add_norm_kernel<TPR, C, RT>, dim3((unsigned)((rows + kGroups - 1) / kGroups)), dim3(kThreads),
-                       0, s, false, a, rows);
+                       0, s, true, a, rows);
 }
 
 template <typename RT>
@@ -376,7 +383,7 @@ static cudaError_t launch_add_norm_rows(const AddNormArgs &a, long long rows, bo
     static PerDeviceOnce once;
     const cudaError_t e = any_smem_limit(reinterpret_cast<const void *>(add_norm_any_kernel<RT>), once);
     if (e != cudaSuccess) return e;
-    return launch_kernel(add_norm_any_kernel<RT>, dim3((unsigned)rows), dim3(kAnyThreads), (size_t)a.D * 4, s, false, a);
+    return launch_kernel(add_norm_any_kernel<RT>, dim3((unsigned)rows), dim3(kAnyThreads), (size_t)a.D * 4, s, true, a);
   }
   const RowShape r = row_shape(a.D);
   switch (r.tpr * 8 + r.c) {
@@ -403,7 +410,7 @@ static cudaError_t launch_norm_gate_rows(const NormGateArgs &a, bool vec, cudaSt
     static PerDeviceOnce once;
     const cudaError_t e = any_smem_limit(reinterpret_cast<const void *>(norm_gate_any_kernel), once);
     if (e != cudaSuccess) return e;
-    return launch_kernel(norm_gate_any_kernel, dim3((unsigned)a.rows), dim3(kAnyThreads), (size_t)a.D * 4, s, false, a);
+    return launch_kernel(norm_gate_any_kernel, dim3((unsigned)a.rows), dim3(kAnyThreads), (size_t)a.D * 4, s, true, a);
   }
   const int sms = device_sm_count();
   const RowShape r = row_shape(a.D);
