@@ -112,10 +112,11 @@ def test_segments_of_long_sequences(lens, init):
 @pytest.mark.parametrize("lens,H,packed", [
     ([1250] * 5, 40, False), ([1250] * 51, 3, False), ([1250] * 5, 40, True), ([600] * 40 + [3000, 512], 5, True),
     ([900, 0, 2047, 1, 513, 1400, 130, 1664, 700, 1025], 24, True),
+    ([3000, 0, 2047, 1, 5130, 1400, 130, 1664, 2700, 1025], 24, True), ([9000] + [700, 20] * 12, 20, True),
 ])
 def test_more_sequences_than_blocks(lens, H, packed, K, V):
-    """More sequences and heads than SMs, and not a multiple: where lengths are equal, a block goes on with
-    the state of another."""
+    """More sequences and heads than SMs, and not a multiple: to even out the blocks' shares, a block goes on
+    with the state of another."""
     if packed:
         d = make(1, 0, H, H, K, V, seed=H + K, lens=lens, token=True)
     else:
