@@ -341,16 +341,17 @@ static cudaError_t any_smem_limit(const void *kernel, PerDeviceOnce &once) {
 }
 
 // Threads per row and 16-byte chunks per thread of a row of D values: one chunk up to 2048 values, two up to
-// 4096, four beyond, and as few idle threads as multiples of 64 allow. (16384 rows of add_norm on one GB300:
-// 2048 bf16 values 46.7 us with one chunk, 49.8 with two; 4096 values, fp32 residual, all parts, 136 us
-// with two, 152 with one; 10744 rows of 2880 values 64 us with 192 threads, 72 with 256.)
+// 6144, four beyond, and as few idle threads as multiples of 64 allow. (add_norm on one GB300, microseconds:
+// 16384 rows of 2048 bf16 values, without gate and post norm, 46.7 with one chunk, 49.8 with two; 16384 of 4096, fp32
+// residual, all parts, 136 with two, 152 with one; 8000 of 6144, bf16 residual, all parts, 77.5 with two, 84.2 with
+// four; 4096 of 8192 59.1 and 57.3; 10744 of 2880 64 with 192 threads, 72 with 256.)
 struct RowShape { int tpr, c; };
 static RowShape row_shape(int D) {
   const int n = D / 8;
   if (n <= 8) return {8, 1};
   if (n <= 16) return {16, 1};
   if (n <= 32) return {32, 1};
-  const int c = n <= 256 ? 1 : n <= 512 ? 2 : 4;
+  const int c = n <= 256 ? 1 : n <= 768 ? 2 : 4;
   return {(n + 64 * c - 1) / (64 * c) * 64, c};
 }
 
@@ -396,7 +397,8 @@ static cudaError_t launch_add_norm_rows(const AddNormArgs &a, long long rows, bo
     case 256 * 8 + 1: return launch_add_norm<256, 1, RT>(a, rows, s);
     case 192 * 8 + 2: return launch_add_norm<192, 2, RT>(a, rows, s);
     case 256 * 8 + 2: return launch_add_norm<256, 2, RT>(a, rows, s);
-    case 192 * 8 + 4: return launch_add_norm<192, 4, RT>(a, rows, s);
+    case 320 * 8 + 2: return launch_add_norm<320, 2, RT>(a, rows, s);
+    case 384 * 8 + 2: return launch_add_norm<384, 2, RT>(a, rows, s);
     case 256 * 8 + 4: return launch_add_norm<256, 4, RT>(a, rows, s);
     case 320 * 8 + 4: return launch_add_norm<320, 4, RT>(a, rows, s);
     case 384 * 8 + 4: return launch_add_norm<384, 4, RT>(a, rows, s);
@@ -424,7 +426,8 @@ static cudaError_t launch_norm_gate_rows(const NormGateArgs &a, bool vec, cudaSt
     case 256 * 8 + 1: return launch_norm_gate<256, 1>(a, s, sms);
     case 192 * 8 + 2: return launch_norm_gate<192, 2>(a, s, sms);
     case 256 * 8 + 2: return launch_norm_gate<256, 2>(a, s, sms);
-    case 192 * 8 + 4: return launch_norm_gate<192, 4>(a, s, sms);
+    case 320 * 8 + 2: return launch_norm_gate<320, 2>(a, s, sms);
+    case 384 * 8 + 2: return launch_norm_gate<384, 2>(a, s, sms);
     case 256 * 8 + 4: return launch_norm_gate<256, 4>(a, s, sms);
     case 320 * 8 + 4: return launch_norm_gate<320, 4>(a, s, sms);
     case 384 * 8 + 4: return launch_norm_gate<384, 4>(a, s, sms);
