@@ -382,7 +382,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
       if (nch > 0) load_decays(it, h, 0);
       // The state that the state warps need when they get to this item, some chunks from now. (64 x 512 tokens of
       // 64 heads, without and with: fp32 states 486 and 480 us, bf16 502 and 485, bf16 [K, V] 587 and 500.)
-      if (!AGG && init && it.seg == 0 && umma::elect_one())
+      if (!AGG && init && it.n_seg == 1 && umma::elect_one())
         umma::prefetch_l2_bulk(init + (long long)(it.seq * p.H + h) * state_bytes, state_bytes);
       return true;
     }, [&](const LaItem &it, int h, int c, int nch, int n) {
@@ -770,15 +770,17 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
     };
     for_chunks(
         [&](const LaItem &it, int h, int nch) {
-          const bool other = SHARE && (it.part & kLaFromOther);
-          if (AGG || (it.seg == 0 && !p.init && !other) || !has_v) {
+          // Only a sequence in one piece reads p.init here, and writes final_state after it: they may be one
+          // buffer, and between the segments of a sequence, on different CTAs, nothing else orders the two.
+          const bool other = SHARE && (it.part & kLaFromOther), first = it.seg == 0 && !other;
+          if (AGG || (first && !p.init) || !has_v) {
 #pragma unroll
             for (int j = 0; j < KH; ++j) S[j] = 0.f;
-          } else if (it.seg == 0 && !other) {
+          } else if (first && it.n_seg == 1) {
             la_state_move<K, V, KH, false>(p, it.seq, h, (warp & 3) * 32, half * KH, S, patch);
           } else {
             if (other && !hand_wait(ms.cta - 1)) return false;
-            const float *src = other ? hand_block(ms.cta - 1) : seg_block(it.slot - 1, h);
+            const float *src = other ? hand_block(ms.cta - 1) : seg_block(first ? it.slot + it.n_seg - 1 : it.slot - 1, h);
 #pragma unroll
             for (int j = 0; j < KH / 4; ++j) {
               const float4 f = __ldcg(reinterpret_cast<const float4 *>(src + la_seg_index<K, V>(half, row, j)));
@@ -895,7 +897,8 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
 }
 
 // Start states of the segments: chains, over the segments of a sequence, what each segment adds.
-// One thread per four state values; segment g's block is read and then holds the start of g + 1. Bound by
+// One thread per four state values; segment g's block is read and then holds the start of g + 1, and the
+// last segment's block, which adds to none, the start of the first: the initial state in fp32. Bound by
 // latency: 6.8 us for nine segments of 16 heads at K = V = 128 (8 MB read), with eight loads of a thread in
 // flight; a launch of it with nothing to combine takes 4 us.
 template <int K, int V>
@@ -922,6 +925,8 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const LaProblem p) {
       S[e] = (p.flags & kStateBf16) ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.init)[i])
                                     : static_cast<const float *>(p.init)[i];
     }
+    reinterpret_cast<float4 *>(p.seg_state + ((long long)(slot0 + n - 1) * p.H + h) * (K * V))[x] =
+        make_float4(S[0], S[1], S[2], S[3]);
   }
   constexpr int kAhead = 8;   // blocks whose loads are in flight together
   for (int g0 = 0; g0 + 1 < n; g0 += kAhead) {

@@ -27,8 +27,8 @@ struct LaProblem {
   const int32_t *cu;             // [N+1] or null
   __nv_bfloat16 *o;              // [B,T,H,V]
   // Segments (n_seg > 1): slot s of head h holds at seg_state + (s H + h) K V first the state that
-  // the segment adds when started from zero, after the combine the start state of segment s + 1;
-  // seg_decay[s H + h] is the product of its decays.
+  // the segment adds when started from zero, after the combine the start state of segment s + 1; the
+  // slot of a sequence's last segment that of its first. seg_decay[s H + h] is the product of its decays.
   float *seg_state;
   float *seg_decay;
   // Varlen, by the schedule kernel: the work list, the segments formed ahead first; how many items, how
