@@ -1144,7 +1144,8 @@ static LaPlan la_plan(int T, int H, int K, int V, int N, bool varlen) {
   r.seg_chunks = la_segment_chunks((long long)N * H, nc_mean, K, V, sms, false);
   if (r.seg_chunks >= nc_mean) r.seg_chunks = std::max(nc_mean, std::max(share, 8));
   r.n_seg = 1;
-  r.multi = std::min((long long)N, (long long)T / ((long long)r.seg_chunks * kLaChunk));
+  // (more than one segment needs a token past the first one's)
+  r.multi = std::min((long long)N, std::max(T - 1, 0) / ((long long)r.seg_chunks * kLaChunk));
   r.segments = r.multi > 0;
   r.slots = (long long)T / ((long long)r.seg_chunks * kLaChunk) + 2ll * N;
   return r;
