@@ -1013,31 +1013,46 @@ __global__ void __launch_bounds__(kLaSchedThreads) la_schedule_kernel(const LaPr
     return;
   }
   if (tid == 0) *p.flag = kDevOk;
+  const int seg_len = p.seg_chunks * kLaChunk;
+  auto put = [&](int pos, int seq, int t0, int len, int g, int n, int slot0) {
+    LaItem it;
+    it.seq = seq;
+    it.b = 0;
+    it.seg = g;
+    it.n_seg = n;
+    it.slot = slot0 + g;
+    it.t0 = g ? t0 + g * seg_len : t0;
+    it.len = g < n - 1 ? seg_len : len - (it.t0 - t0);
+    it.part = 0;
+    p.items[pos] = it;
+  };
   const int longest = min(p.seg_chunks, (p.T + kLaChunk - 1) / kLaChunk);
   const int per_bin = longest / kLaSchedBins + 1;   // chunk counts per bin; bins in descending order
   auto bin_of = [&](int chunks) { return (longest - chunks) / per_bin; };
-  // slots of the sequences' segments; how many segments are formed ahead, how many sequences have any
-  int slots = 0, ahead = 0, multi = 0;
+  // how many segments are formed ahead, how many sequences have any
+  int ahead = 0, multi = 0;
   for (int base = 0; base < N; base += kLaSchedThreads) {
     const int i = base + tid;
-    int n = 0;
+    int n = 1, t0 = 0, len = 0;
     if (i < N) {
-      const int nc = (cu[i + 1] - cu[i] + kLaChunk - 1) / kLaChunk;
+      t0 = cu[i];
+      len = cu[i + 1] - t0;
+      const int nc = (len + kLaChunk - 1) / kLaChunk;
       n = max(1, (nc + p.seg_chunks - 1) / p.seg_chunks);
       atomicAdd(&s_bins[bin_of(nc - (n - 1) * p.seg_chunks)], 1);
     }
-    int total, many;
-    const int before = block_exclusive_sum(n, s_part, total);
-    const int rank = block_exclusive_sum(n > 1, s_part, many);
-    if (i < N) p.slot0[i] = slots + before;
-    if (n > 1) p.multi[multi + rank] = i;
-    ahead += total - min(N - base, kLaSchedThreads);
-    slots += total;
+    int more, many;
+    const int before = ahead + block_exclusive_sum(n - 1, s_part, more);
+    const int rank = multi + block_exclusive_sum(n > 1, s_part, many);
+    if (i < N) p.slot0[i] = before + rank;   // the sequences before that have slots have one more than are formed ahead
+    if (n > 1) p.multi[rank] = i;
+    for (int g = 0; g < n - 1; ++g) put(before + g, i, t0, len, g, n, before + rank);
+    ahead += more;
     multi += many;
   }
   if (tid == 0) {
-    p.slot0[N] = slots;
-    p.counts[0] = slots;
+    p.slot0[N] = ahead + multi;
+    p.counts[0] = N + ahead;
     p.counts[1] = ahead;
     p.counts[2] = multi;
   }
@@ -1049,34 +1064,21 @@ __global__ void __launch_bounds__(kLaSchedThreads) la_schedule_kernel(const LaPr
   s_bins[2 * tid] = at;
   s_bins[2 * tid + 1] = at + x0;
   __syncthreads();
-  const int seg_len = p.seg_chunks * kLaChunk;
   for (int i = tid; i < N; i += kLaSchedThreads) {
-    const int t0 = cu[i], len = cu[i + 1] - t0, slot0 = p.slot0[i];
+    const int t0 = cu[i], len = cu[i + 1] - t0;
     const int nc = (len + kLaChunk - 1) / kLaChunk, n = max(1, (nc + p.seg_chunks - 1) / p.seg_chunks);
-    for (int g = 0; g < n; ++g) {
-      LaItem it;
-      it.seq = i;
-      it.b = 0;
-      it.seg = g;
-      it.n_seg = n;
-      it.slot = slot0 + g;
-      it.t0 = g ? t0 + g * seg_len : t0;
-      it.len = g < n - 1 ? seg_len : len - (it.t0 - t0);
-      it.part = 0;
-      // (a sequence's segments before its last have slot0 - i segments formed ahead before them)
-      const int pos = g < n - 1 ? slot0 - i + g : atomicAdd(&s_bins[bin_of(nc - (n - 1) * p.seg_chunks)], 1);
-      p.items[pos] = it;
-    }
+    put(atomicAdd(&s_bins[bin_of(nc - (n - 1) * p.seg_chunks)], 1), i, t0, len, n - 1, n, p.slot0[i]);
   }
 }
 
 // ---------------------------------------------------------------------------------- host
 
-// How a call is cut: chunks per segment, segments per sequence (fixed length) and the slots that
-// the workspace holds.
+// How a call is cut: chunks per segment, segments per sequence (fixed length), and how many items and
+// segment states the workspace holds.
 struct LaPlan {
   int seg_chunks, n_seg;
-  long long slots;
+  long long items;     // segments of all sequences: at most so many
+  long long slots;     // segments of the sequences of more than one: at most so many
   bool segments;       // whether any sequence may have more than one segment
   long long multi;     // how many may
   int shared;          // CTAs of a call that may hand a state over, or 0
@@ -1131,9 +1133,9 @@ static LaPlan la_plan(int T, int H, int K, int V, int N, bool varlen) {
     r.seg_chunks = la_segment_chunks((long long)N * H, nc, K, V, sms, true);
     r.n_seg = (nc + r.seg_chunks - 1) / r.seg_chunks;
     r.segments = r.n_seg > 1;
-    r.slots = (long long)N * r.n_seg;
+    r.items = r.slots = (long long)N * r.n_seg;
     r.multi = N;
-    const long long items = r.slots * H, rounds = (items + sms - 1) / sms;
+    const long long items = r.items * H, rounds = (items + sms - 1) / sms;
     if (items > sms && (rounds - (double)items / sms) * r.seg_chunks > kLaShareChunks) r.shared = sms;
     return r;
   }
@@ -1144,10 +1146,12 @@ static LaPlan la_plan(int T, int H, int K, int V, int N, bool varlen) {
   r.seg_chunks = la_segment_chunks((long long)N * H, nc_mean, K, V, sms, false);
   if (r.seg_chunks >= nc_mean) r.seg_chunks = std::max(nc_mean, std::max(share, 8));
   r.n_seg = 1;
-  // (more than one segment needs a token past the first one's)
-  r.multi = std::min((long long)N, std::max(T - 1, 0) / ((long long)r.seg_chunks * kLaChunk));
+  // Each segment but a sequence's last is full, and has a token behind it.
+  const long long ahead = std::max(T - 1, 0) / ((long long)r.seg_chunks * kLaChunk);
+  r.multi = std::min((long long)N, ahead);
   r.segments = r.multi > 0;
-  r.slots = (long long)T / ((long long)r.seg_chunks * kLaChunk) + 2ll * N;
+  r.items = N + ahead;
+  r.slots = r.multi + ahead;
   return r;
 }
 
@@ -1167,7 +1171,7 @@ static LaScratch la_scratch(const LaPlan &pl, int H, int K, int V, int N, bool v
     s.multi = off;
     off = up(off + 4 * (size_t)pl.multi);
     s.items = off;
-    off = up(off + sizeof(LaItem) * (size_t)pl.slots);
+    off = up(off + sizeof(LaItem) * (size_t)pl.items);
   }
   if (pl.segments) {
     s.decay = off;
@@ -1200,7 +1204,6 @@ static cudaError_t launch_la_t(const LaProblem &p, const LaMaps &maps, long long
 
 template <int K, int V>
 static cudaError_t launch_la(const LaProblem &p, const LaMaps &maps, const LaPlan &pl, cudaStream_t s) {
-  const long long items = p.cu ? pl.slots : (long long)p.N * pl.n_seg;
   // Every launch overlaps the end of the kernel ahead, the first one the caller's: 128 tokens of two heads take
   // 7.2 us from one call to the next instead of 10.2.
   if (p.cu) {
@@ -1212,13 +1215,13 @@ static cudaError_t launch_la(const LaProblem &p, const LaMaps &maps, const LaPla
     if (e != cudaSuccess) return e;
   }
   if (pl.segments) {
-    cudaError_t e = launch_la_t<K, V, true>(p, maps, items, s);
+    cudaError_t e = launch_la_t<K, V, true>(p, maps, pl.items, s);
     if (e == cudaSuccess)
       e = launch_kernel(la_combine_kernel<K, V>, dim3((unsigned)(pl.multi * p.H), K * V / 1024), dim3(256), 0, s, true, p);
     if (e != cudaSuccess) return e;
   }
-  return pl.shared ? launch_la_t<K, V, false, true>(p, maps, items, s)
-                   : launch_la_t<K, V, false>(p, maps, items, s);
+  return pl.shared ? launch_la_t<K, V, false, true>(p, maps, pl.items, s)
+                   : launch_la_t<K, V, false>(p, maps, pl.items, s);
 }
 
 static bool la_sizes_ok(int B, int T, int Hk, int H, int K, int V, int N) {
@@ -1266,7 +1269,7 @@ kda_status_t kda_la_fwd(const void *q, const void *k, const void *v, const float
   if ((double)B * T * H * std::max(K, V) > 9.0e15 || T > 2147480000) return KDA_ERR_UNSUPPORTED;
   const bool varlen = cu_seqlens != nullptr;
   const LaPlan pl = la_plan(T, H, K, V, num_seqs, varlen);
-  if ((double)std::max(pl.slots, (long long)num_seqs) * H > 2.0e9) return KDA_ERR_UNSUPPORTED;
+  if ((double)(pl.items + (varlen ? num_seqs : 0)) * H > 2.0e9) return KDA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return KDA_OK;
   const LaScratch L = la_scratch(pl, H, K, V, num_seqs, varlen);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -12,7 +12,7 @@ struct LaItem {
   int seq;
   int t0, len;        // tokens [t0, t0 + len) of batch row b
   int b;
-  int slot;           // index of its segment among all segments
+  int slot;           // index of its segment among those of sequences of more than one
   int seg, n_seg;     // segment of the sequence, number of them
   int part;           // while a CTA has it: kLaFromOther, kLaToOther
 };
@@ -32,8 +32,8 @@ struct LaProblem {
   float *seg_state;
   float *seg_decay;
   // Varlen, by the schedule kernel: the work list, the segments formed ahead first; how many items, how
-  // many of them are formed ahead, and how many sequences have such; the first slot of each sequence
-  // [N + 1]; the sequences of more than one segment.
+  // many of them are formed ahead, and how many sequences have such; the first slot of each sequence that
+  // has more than one segment [N + 1]; those sequences.
   LaItem *items;
   int32_t *counts;
   int32_t *slot0;

@@ -21,3 +21,11 @@ def built():
 def test_packed_calls_without_a_second_segment_need_a_schedule_alone(T, H, N):
     """One sequence of all tokens fits one segment of these calls, so that nothing is formed ahead."""
     assert kda.la_workspace_size(1, T, H, 128, 128, N, True) < STATE + 64 * N
+
+
+@pytest.mark.parametrize("T,H,N,blocks", [(70000, 64, 512, 2), (200000, 8, 4000, 16), (9000, 32, 2000, 0)])
+def test_packed_calls_hold_no_states_of_sequences_in_one_segment(T, H, N, blocks):
+    """However many sequences there are: `blocks` states per head are what the tokens can fill segments with, twice."""
+    size = kda.la_workspace_size(1, T, H, 128, 128, N, True)
+    assert size < blocks * H * (STATE + 4) + 64 * (N + 16)
+    assert size >= blocks // 2 * H * STATE

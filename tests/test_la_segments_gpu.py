@@ -1,4 +1,4 @@
-"""la_fwd on sequences that are cut into segments: states in place."""
+"""la_fwd on sequences that are cut into segments: states in place, and a workspace of the size asked for."""
 from __future__ import annotations
 
 import pytest
@@ -85,4 +85,24 @@ def test_final_state_in_place_while_some_multiprocessors_are_taken(shape):
     torch.cuda.synchronize()
     for o, st, _ in got:
         assert torch.equal(o, want[0]) and torch.equal(st, want[1])
+    assert kda.device_status() == 0
+
+
+LONG_AND_SHORT = [9000] + [0, 1, 40, 300] * 60 + [128 * 9 + 1, 5000] + [17] * 1100 + [4000]   # more than one tile of the schedule
+
+
+@pytest.mark.parametrize("lens,H", PACKED + [(LONG_AND_SHORT, 4), ([1024], 16), ([1025], 64), ([5, 1020], 64)])
+def test_a_workspace_of_exactly_the_size_asked_for(lens, H):
+    """4 KB of guard bytes around it; the bits of a call that allocates its own, and of the next call in the same one."""
+    d = make(1, 0, 1, H, 64, 128, seed=7, lens=lens, token=True)
+    call, buffers = calls(d)
+    want = check(d, "own workspace") if sum(lens) * H < 100000 else call(*buffers())
+    size = kda.la_workspace_size(1, sum(lens), H, 64, 128, len(lens), True)
+    buf = torch.full((size + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        o, init, final = buffers()
+        kda.la_fwd(d["q"], d["k"], d["v"], d["log_decay"], initial_state=init, output_final_state=True,
+                   cu_seqlens=d["cu_seqlens"], out=o, final_state=final, workspace=buf[4096:4096 + size])
+        assert torch.equal(o, want[0]) and torch.equal(final, want[1])
+        assert bool((buf[:4096] == 0xA5).all()) and bool((buf[-4096:] == 0xA5).all())
     assert kda.device_status() == 0
