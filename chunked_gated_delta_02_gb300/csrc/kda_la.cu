@@ -16,7 +16,10 @@
 // R_i = max(G_i, -64 ln 2) takes the row's decay out of P, so that M2 and M3 can add into one
 // accumulator and an element of P costs one factor of its column, exp(-G_j). Where the decay of a
 // chunk goes below 2^-64, G_i - G_j - R_i stays within (-inf, 64 ln 2] and is formed pairwise; rows
-// that far down take 2^-64 Q S instead of less, which is below the rounding of anything else.
+// that far down take 2^-64 Q S instead of less, which is below the rounding of anything else. Positive
+// log decays may lead back up: with m_i the least G_j of j <= i, G_i - G_j - R_i would reach -m_i where
+// G_i > -64 ln 2, and R_i is raised to G_i - m_i - 96 ln 2. Such rows take exp(G_i - m_i) 2^-96 Q S, at
+// most 2^-32 Q S for growths up to 2^64, where token argmin m counts 2^96 times as much.
 //
 // What is rounded: q, k and v are exact (bf16 inputs). P and the copy of S that M2 reads are bf16,
 // like the output they go to: each adds about as much error as the rounding of o itself. The state
@@ -68,6 +71,7 @@ constexpr unsigned kLaWaitLimit = 4000000000u;   // ~2 s of SM clocks per wait
 constexpr float kLaMinLog2 = -126.0f;
 // Row decays below 2^-64 stay in P (see above): 2^64 leaves the scores and values as much range again.
 constexpr float kLaRowLog2 = -64.0f;
+constexpr float kLaMostLog2 = 96.0f;   // the largest G_i - G_j - R_i
 
 // Decay factors of one chunk.
 struct LaGate {
@@ -77,9 +81,21 @@ struct LaGate {
   float cf[kLaChunk];   // decay from token j to the end of its 32-token block; 0 past the sequence
   float bf[4];          // decay from the end of 32-token block c to the chunk's end
   float gamma;          // decay of the whole chunk
-  int weak;
+  int weak;             // 1: weak; 0: not; -1: not, and some token's log decay is positive
   float pad[2];
 };
+
+// G_i - R_i of a chunk that is not weak.
+__device__ __forceinline__ float la_row_shift(const LaGate &g, int row, int weak) {
+  float x = fminf(g.G[row] - kLaRowLog2, 0.f);
+  if (weak < 0) {
+    float least = 0.f;
+#pragma unroll 1
+    for (int j = 0; j <= row; ++j) least = fminf(least, g.G[j]);
+    x = fminf(x, least + kLaMostLog2);
+  }
+  return x;
+}
 
 struct LaMisc {
   // per stage: q and k loaded, consumed; v loaded, consumed; decay factors written (consumed with q and
@@ -442,7 +458,15 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
         const float later = __shfl_down_sync(0xffffffffu, after, 1);
         const float tail = (lane & 7) == 7 ? 0.f : later;
         LaGate &g = gates[st];
-        const bool weak = __shfl_sync(0xffffffffu, incl, 31) >= kLaRowLog2;   // so are all sums, for decays <= 1
+        // The least of the sums is the last one, unless a log decay is positive.
+        float least = __shfl_sync(0xffffffffu, incl, 31);
+        const bool rises = __any_sync(0xffffffffu, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) > 0.f);
+        if (rises) {
+          least = before + fminf(fminf(pre[0], pre[1]), fminf(pre[2], pre[3]));
+#pragma unroll
+          for (int m = 1; m < 32; m <<= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, m));
+        }
+        const bool weak = least >= kLaRowLog2;
         float G[4], cf[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -459,7 +483,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           g.bf[2] = ex2_approx(b3);
           g.bf[3] = 1.f;
           g.gamma = ex2_approx(b0 + b1 + b2 + b3);
-          g.weak = weak;
+          g.weak = weak ? 1 : rises ? -1 : 0;
         }
         __syncwarp();
         const int keep = per_token || L < kLaChunk ? -1 : h;
@@ -683,8 +707,9 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
       const int st = n % kStages;
       if (!wait(&ms.gate[st], (uint32_t)((n / kStages) & 1))) return false;
       const LaGate &g = gates[st];
-      const bool weak = g.weak != 0;
-      const float Gr = weak ? 0.f : g.G[row] - fmaxf(g.G[row], kLaRowLog2);   // G_i - R_i
+      const int mode = g.weak;
+      const bool weak = mode > 0;
+      const float Gr = weak ? 0.f : la_row_shift(g, row, mode);   // G_i - R_i
       if (!wait(&ms.p_raw, (uint32_t)(n & 1))) return false;
       // block c of P goes to columns 16 c .. of the scores, block c / 2 of them: read by then
 #pragma unroll 1
@@ -802,7 +827,8 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           float f = 0.f;   // scale exp(R_i) of this thread's token row
           if constexpr (!AGG) {
             const float G = gates[st].G[row];
-            f = p.scale * (gates[st].weak ? rcp_approx(G) : ex2_approx(fmaxf(G, kLaRowLog2)));
+            const int weak = gates[st].weak;
+            f = p.scale * (weak > 0 ? rcp_approx(G) : ex2_approx(G - la_row_shift(gates[st], row, weak)));
           }
           arrive(&ms.empty[st]);   // the factors have been read
           auto new_state = [&] {   // S^T = gamma S^T + D^T

@@ -97,11 +97,12 @@ def la_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.T
     """Linear attention with a decay per head over prompts, chunked.
 
     q, k: bf16 [B,T,Hk,K], Hk dividing the H heads of v; v: bf16 [B,T,H,V]; log_decay: fp32 [H], or
-    [B,T,H] for a decay per token, <= 0. initial_state: [N,H,V,K] ("vk") or [N,H,K,V] ("kv"), fp32
-    or bf16, or None; cu_seqlens: int32 [N+1] of packed sequences (then B must be 1) or None.
-    state_dtype: dtype of the final state when there is no initial_state (default fp32; with an
-    initial_state, its dtype). Strides of q, k and v must be multiples of 8 elements and their bases
-    16-byte aligned. Returns (o bf16 [B,T,H,V], final_state or None). The call can be captured in a
+    [B,T,H] for a decay per token, <= 0 (or positive where no run of up to 128 tokens sums to more
+    than 44). initial_state: [N,H,V,K] ("vk") or [N,H,K,V] ("kv"), fp32 or bf16, or None;
+    cu_seqlens: int32 [N+1] of packed sequences (then B must be 1) or None. state_dtype: dtype of the
+    final state when there is no initial_state (default fp32; with an initial_state, its dtype).
+    Strides of q, k and v must be multiples of 8 elements and their bases 16-byte aligned. Returns
+    (o bf16 [B,T,H,V], final_state or None). The call can be captured in a
     CUDA graph when a `workspace` tensor is passed.
     """
     if state_dtype not in (None, torch.float32, torch.bfloat16):

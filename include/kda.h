@@ -394,7 +394,8 @@ KDA_API kda_status_t kda_step(const void *q, const void *k, const void *v, const
  *                  logarithms, <= 0. Values below -126 ln 2 (a decay below the
  *                  smallest normal number, -inf included) count as that.
  *                  Positive values are taken as they are, and are meaningful
- *                  while exp of their sum over 128 tokens is finite.
+ *                  while no run of up to 128 tokens sums to more than 44 (a
+ *                  growth by 2^64), whatever decays come before or after it.
  *   initial_state, final_state, cu_seqlens, num_seqs   as in kda_fwd_ex()
  *                  (KDA_STATE_BF16, KDA_STATE_KV); final_state may be
  *                  initial_state.
