@@ -1,4 +1,4 @@
-"""norm_gate and add_norm in the forms that the row length chooses, against fp64.
+"""norm_gate and add_norm in each form that the row length and the number of rows choose, against fp64.
 
 The bounds are those of test_norms_gpu.py.
 """
@@ -49,3 +49,45 @@ def test_add_norm_rows_past_the_prefetch(D, rdt):
     for part in (slice(0, 40), slice(rows - 90, rows)):
         one_y, one_h = check_add(x[part], r[part], w, None, None, 0.5, what=f"{rows} x {D}")
         assert torch.equal(y[part], one_y) and torch.equal(h[part], one_h)
+
+
+def within(y, ref):
+    """test_norms_gpu.within for a bf16 result, on the GPU, with terms of the size of the result."""
+    assert bool(torch.isfinite(y).all())
+    size = ref.abs()
+    arith = 2.0 ** -20 * size
+    _, exponent = torch.frexp((size + arith).clamp(min=2.0 ** -126))
+    bound = torch.ldexp(torch.ones_like(size), exponent - 9) + arith
+    worst = float(((y.double() - ref).abs() / bound).max())
+    assert worst <= 1.0, f"{worst:.2f} of the bound"
+
+
+@pytest.mark.parametrize("D,groups", [(40, 32), (64, 32), (104, 16), (128, 16), (200, 8), (256, 8)])
+@pytest.mark.parametrize("past", [-1, 0, 1, "ragged"])
+@pytest.mark.parametrize("weight,activation,views", [(True, "silu", True), (False, "sigmoid", False), (True, "sigmoid", True)])
+def test_norm_gate_row_counts_around_the_four_row_form(D, groups, past, weight, activation, views):
+    """Groups of threads take four rows each from 24 blocks of `groups` such groups per multiprocessor on. Every row is
+    compared; x and the gate are views of one tensor, or contiguous."""
+    heads = 3
+    rows = torch.cuda.get_device_properties(0).multi_processor_count * 24 * groups * 4
+    rows += 2 * groups + groups // 2 + 1 if past == "ragged" else past
+    if views:
+        rows = -(-rows // heads) * heads if past != -1 else (rows // heads) * heads
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda")
+
+    if views:
+        x, gate = normal(rows // heads, 2, heads, D).bfloat16().unbind(1)
+    else:
+        x, gate = normal(rows, D).bfloat16(), normal(rows, D).bfloat16()
+    w = normal(D) if weight else None
+    y = kda.norm_gate(x, gate, w, activation=activation)
+    assert y.shape == x.shape
+    for part in torch.arange(x.shape[0], device="cuda").chunk(8):
+        a, g = x[part].double(), gate[part].double()
+        ref = a * torch.rsqrt(a.square().mean(-1, keepdim=True) + 1e-6) * torch.sigmoid(g)
+        if activation == "silu":
+            ref = ref * g
+        within(y[part], ref if w is None else ref * w.double())
