@@ -74,6 +74,16 @@ void need(const Tensor &t, const char *name, at::ScalarType dtype, IntArrayRef s
     value_error(std::string(name) + " must have shape " + tuple_text(shape) + ", got " + tuple_text(t.sizes()));
   need_layout(t, name, dtype, dev, contiguous);
 }
+void need_aligned(const Tensor &t, const char *name) {
+  if (reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 != 0) value_error(std::string(name) + " must begin on a 16-byte boundary");
+}
+// A tensor that is read in boxes of 16-byte pieces: its base, and the strides of all dimensions but the last.
+void need_boxes(const Tensor &t, const char *name) {
+  for (int i = 0; i + 1 < t.dim(); ++i)
+    if (t.size(i) > 1 && (t.stride(i) <= 0 || t.stride(i) % 8 != 0))
+      value_error(std::string(name) + " must have strides that are positive multiples of 8, got " + tuple_text(t.strides()));
+  need_aligned(t, name);
+}
 void need_gpu(const Tensor &t, const char *name) {
   if (!t.is_cuda()) value_error(std::string(name) + " must be a CUDA tensor (there is no CPU path)");
 }
@@ -132,6 +142,7 @@ Pool pool(PyObject *state, PyObject *indices, bool kv, int64_t N, int64_t H, int
   p.indices = nullptr;
   const int64_t shape[4] = {p.rows, H, kv ? K : V, kv ? V : K};
   need(t, "state", t.scalar_type(), shape, dev, true);
+  need_aligned(t, "state");
   if (given(indices)) {
     const Tensor &i = as_tensor(indices, "state_indices");
     const int64_t n[1] = {N};
@@ -269,6 +280,9 @@ PyObject *la_fwd(PyObject *const *a) {
   kda_la_strides_t st;
   const int64_t lead[2] = {B, T};
   uint32_t flags = decay_of(decay, lead, x.H, dev, st.log_decay);
+  need_boxes(q, "q");
+  need_boxes(k, "k");
+  need_boxes(v, "v");
   int64_t N = B;
   const int32_t *cu = nullptr;
   if (given(a[7])) {
@@ -288,6 +302,7 @@ PyObject *la_fwd(PyObject *const *a) {
     state_flags(t, kv);
     sdt = t.scalar_type();
     need(t, "initial_state", sdt, ss, dev, true);
+    need_aligned(t, "initial_state");
     init = t.data_ptr();
   }
   flags |= (kv ? KDA_STATE_KV : 0u) | (sdt == at::kBFloat16 ? KDA_STATE_BF16 : 0u);
@@ -295,6 +310,8 @@ PyObject *la_fwd(PyObject *const *a) {
   Tensor fs;
   if (a[6] == Py_True) fs = output(a[10], "final_state", ss, sdt, dev);
   Tensor o = output(a[9], "out", os, at::kBFloat16, dev);
+  if (fs.defined()) need_aligned(fs, "final_state");
+  need_aligned(o, "out");
   Tensor ws;
   if (given(a[8])) {
     ws = as_tensor(a[8], "workspace");
