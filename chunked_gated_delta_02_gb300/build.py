@@ -3,13 +3,15 @@
 Every .cu file under csrc/ is compiled to an object in parallel, then linked
 into chunked_gated_delta_02_gb300/libkda.so; binding.cpp is compiled beside them
 with the host compiler against the installed torch, and linked with libkda.so
-into the extension module _serving. Only one -gencode target is
+into the extension module _serving; where there is no torch, libkda.so is all
+that is built. Only one -gencode target is
 built: compute_103a / sm_103a (the arch-specific variant is needed for the
 tcgen05 and TMA instructions).
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -38,8 +40,9 @@ def sources():
 
 
 def _torch_dir():
-    import torch
-    return os.path.dirname(torch.__file__)
+    """The installed torch's folder, or None."""
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None else os.path.dirname(spec.origin)
 
 
 def _binding_compile(obj):
@@ -64,8 +67,20 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _link(target, deps, command, force):
+    if force or _stale(target, deps):
+        tmp = target + f".tmp{os.getpid()}"
+        r = subprocess.run(command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        if r.returncode != 0:
+            raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
+        os.replace(tmp, target)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile and link libkda.so; returns its path. Raises on a compiler error."""
+    """Compile and link libkda.so, then the binding where torch is installed; returns the library's path.
+
+    Raises on a compiler error; one in the binding leaves the library in place.
+    """
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     headers = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
@@ -82,30 +97,29 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     binding_src = os.path.join(CSRC, "binding.cpp")
     binding_obj = os.path.join(BUILD, "binding.cpp.o")
-    if force or _stale(binding_obj, [binding_src] + headers):
+    with_binding = _torch_dir() is not None
+    if with_binding and (force or _stale(binding_obj, [binding_src] + headers)):
         cmd = _binding_compile(binding_obj)
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((binding_src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    failed = []
+    failed = {}
     for src, pr in procs:
         out, _ = pr.communicate()
         text = out.decode(errors="replace")
         if pr.returncode != 0:
-            failed.append(f"--- {src}\n{text}")
+            failed[src] = f"--- {src}\n{text}"
         elif verbose or ptxas_verbose:
             sys.stderr.write(text)
+    binding_failed = failed.pop(binding_src, None)
     if failed:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
-    for target, deps, command in (
-            (LIB, objs, lambda tmp: [nvcc()] + ARCH + ["-shared", "-Xlinker", "-soname=libkda.so", "-o", tmp] + objs + ["-lcudart"]),
-            (BINDING, [binding_obj, LIB], lambda tmp: _binding_link(binding_obj, tmp))):
-        if force or _stale(target, deps):
-            tmp = target + f".tmp{os.getpid()}"
-            r = subprocess.run(command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-            if r.returncode != 0:
-                raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
-            os.replace(tmp, target)
+        raise RuntimeError("nvcc failed:\n" + "\n".join(failed.values()))
+    _link(LIB, objs, lambda tmp: [nvcc()] + ARCH + ["-shared", "-Xlinker", "-soname=libkda.so", "-o", tmp] + objs + ["-lcudart"],
+          force)
+    if binding_failed:
+        raise RuntimeError("the binding failed to compile:\n" + binding_failed)
+    if with_binding:
+        _link(BINDING, [binding_obj, LIB], lambda tmp: _binding_link(binding_obj, tmp), force)
     return LIB
 
 
