@@ -67,6 +67,18 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _note_torch(path):
+    """Writes which torch and Python the binding is built against, if `path` does not say so yet."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        text = "\n".join((_torch_dir(), sys.version, f.read()))
+    if os.path.exists(path):
+        with open(path) as f:
+            if f.read() == text:
+                return
+    with open(path, "w") as f:
+        f.write(text)
+
+
 def _link(target, deps, command, force):
     if force or _stale(target, deps):
         tmp = target + f".tmp{os.getpid()}"
@@ -97,8 +109,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     binding_src = os.path.join(CSRC, "binding.cpp")
     binding_obj = os.path.join(BUILD, "binding.cpp.o")
+    binding_torch = os.path.join(BUILD, "binding.torch")
     with_binding = _torch_dir() is not None
-    if with_binding and (force or _stale(binding_obj, [binding_src] + headers)):
+    if with_binding:
+        _note_torch(binding_torch)
+    if with_binding and (force or _stale(binding_obj, [binding_src, binding_torch] + headers)):
         cmd = _binding_compile(binding_obj)
         if verbose:
             print(" ".join(cmd), file=sys.stderr)

@@ -50,3 +50,19 @@ def test_an_error_in_a_kernel_is_raised(tree):
     with pytest.raises(RuntimeError, match="one.cu"):
         build.build()
     assert not (tree / "libkda.so").exists()
+
+
+def test_another_torch_builds_the_binding_anew(tree, tmp_path, monkeypatch):
+    build.build()
+    made = {f: os.stat(tree / f).st_mtime_ns for f in ("libkda.so", "_serving.so")}
+    real, other = build._torch_dir(), tmp_path / "torch"
+    other.mkdir()
+    for name in ("include", "lib"):
+        (other / name).symlink_to(os.path.join(real, name))
+    (other / "version.py").write_text("__version__ = '0.0.1'\n")
+    monkeypatch.setattr(build, "_torch_dir", lambda: str(other))
+    build.build()
+    after = {f: os.stat(tree / f).st_mtime_ns for f in made}
+    assert after["libkda.so"] == made["libkda.so"] and after["_serving.so"] > made["_serving.so"]
+    build.build()
+    assert after == {f: os.stat(tree / f).st_mtime_ns for f in made}
