@@ -289,11 +289,13 @@ __device__ __forceinline__ uint32_t mbar_try_wait(uint64_t *bar, uint32_t parity
       : "memory");
   return ok;
 }
-// Whether phase `parity` of `bar` is complete, without suspending the thread.
 // Asks for `bytes` (a multiple of 16) of global memory at the 16-byte aligned p to be brought into L2.
 __device__ __forceinline__ void prefetch_l2_bulk(const void *p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
+// A flag in global memory between blocks of one launch. Data, __threadfence() and __syncwarp() before one
+// lane's st_release; another block's lane that reads it by ld_acquire, and what its warp reads after its vote
+// on the answer, see that data.
 __device__ __forceinline__ int ld_acquire(const int *p) {
   int x;
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
@@ -302,6 +304,7 @@ __device__ __forceinline__ int ld_acquire(const int *p) {
 __device__ __forceinline__ void st_release(int *p, int x) {
   asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(x) : "memory");
 }
+// Whether phase `parity` of `bar` is complete, without suspending the thread.
 __device__ __forceinline__ uint32_t mbar_test(uint64_t *bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
