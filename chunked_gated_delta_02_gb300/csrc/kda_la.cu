@@ -791,6 +791,7 @@ la_kernel(const LaProblem p, const __grid_constant__ LaMaps maps) {
           ok = !*(volatile int *)&ms.err;
         }
       }
+      __syncwarp();   // the vote orders no memory: the other lanes' reads of the state come after the flag's by this
       return (bool)__all_sync(0xffffffffu, ok);
     };
     for_chunks(

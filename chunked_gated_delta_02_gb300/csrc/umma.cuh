@@ -293,9 +293,9 @@ __device__ __forceinline__ uint32_t mbar_try_wait(uint64_t *bar, uint32_t parity
 __device__ __forceinline__ void prefetch_l2_bulk(const void *p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
-// A flag in global memory between blocks of one launch. Data, __threadfence() and __syncwarp() before one
-// lane's st_release; another block's lane that reads it by ld_acquire, and what its warp reads after its vote
-// on the answer, see that data.
+// A flag in global memory between blocks of one launch. The writer: a warp's data, __threadfence() and
+// __syncwarp(), then one lane's st_release. The reader: one lane's ld_acquire, then __syncwarp(), after
+// which the whole warp sees that data.
 __device__ __forceinline__ int ld_acquire(const int *p) {
   int x;
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
