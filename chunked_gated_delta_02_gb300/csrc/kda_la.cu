@@ -42,7 +42,7 @@
 //
 // Bound: a chunk of one head moves 128 KiB at K = V = 128, 2.9 us of an SM's share of the measured
 // bandwidth, against 48 tensor-core steps of 64 clocks, 1.6 us: memory bandwidth, where every SM has work.
-// Measured: 4 x 4096 tokens of 64 heads 187 us, 5.8 TB/s, 85% of the copy bandwidth. Alone on its SM a
+// Measured: 4 x 4096 tokens of 64 heads 188 us, 5.7 TB/s, 85% of the copy bandwidth. Alone on its SM a
 // chunk takes 2.75 us, whatever the other SMs do, and few sequences and heads are bound by that: scores ->
 // P -> O -> next scores and D -> S -> O -> next D are two loops of about 5200 clocks, of which the products
 // take 3100. What keeps them short: V' and P in separate warps; q, k and v released on their own; a state's
